@@ -21,11 +21,21 @@ Operations (gemm_dense_int8.rs launcher page):
 * :func:`silu_mul`, :func:`requant_silu_a`, :func:`proj_silu` -- the SiLU.mul
   quantiser (``W8a8Kernels::quant_silu``) and the down projection from gate
   and up activations.
+
+Integer 4-bit weights with group scales, and mixtures of experts over them:
+
+* :func:`w4g_proj` -- the projection on such a weight as stored.
+* :func:`w4g_proj_grouped` -- the same, rows grouped by expert.
+* :func:`moe_route`, :func:`moe_combine` -- the router that makes the groups
+  and the weighted sum of the experts' rows.
+* :func:`w4g_moe_mlp` -- the expert MLP that runs them together.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import Any, NamedTuple
 
 __all__ = [
     "BsrError",
@@ -62,6 +72,14 @@ __all__ = [
     "requant_silu_a",
     "proj_silu_scratch_bytes",
     "proj_silu",
+    "w4g_proj",
+    "w4g_proj_grouped",
+    "MoeRoute",
+    "moe_route_scratch_bytes",
+    "moe_route",
+    "moe_combine",
+    "w4g_moe_mlp_scratch_bytes",
+    "w4g_moe_mlp",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -85,6 +103,16 @@ STATUS_NAMES = {
 # (name, restype, argtypes) of every exported symbol, mirroring include/bsr.h
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+
+
+class _W4gWeight(ctypes.Structure):
+    """bsr_w4g_weight of include/bsr.h."""
+
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("scale_type", ctypes.c_int), ("group", ctypes.c_int)]
+
+
+_W = ctypes.POINTER(_W4gWeight)
 SIGNATURES = [
     ("bsr_abi_version", ctypes.c_int, []),
     ("bsr_last_error", ctypes.c_char_p, []),
@@ -120,6 +148,15 @@ SIGNATURES = [
     ("bsr_requant_silu_a", ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _P]),
     ("bsr_proj_silu_scratch_bytes", ctypes.c_size_t, [_I64, _I64]),
     ("bsr_proj_silu", ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    ("bsr_w4g_proj", ctypes.c_int, [_P, _W, _P, _I64, _I64, _I64, _P]),
+    ("bsr_w4g_proj_grouped", ctypes.c_int, [_P, _I64, _P, _P, _W, _P, _I64, _I64, _I64, _I64, _P]),
+    ("bsr_moe_route_scratch_bytes", ctypes.c_size_t, [_I64, _I64]),
+    ("bsr_moe_route", ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_uint, _P, _P, _P, _P, _P, _P,
+                                     ctypes.c_size_t, _P]),
+    ("bsr_moe_combine", ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    ("bsr_w4g_moe_mlp_scratch_bytes", ctypes.c_size_t, [_I64, _I64, _I64, _I64, _I64]),
+    ("bsr_w4g_moe_mlp", ctypes.c_int, [_P, _P, ctypes.c_int, _W, _W, _W, _P, _P, _I64, _I64, _I64, ctypes.c_uint,
+                                       _I64, _I64, _P, ctypes.c_size_t, _P]),
 ]
 
 
@@ -753,3 +790,252 @@ def gemm_block_m(m: int, n: int) -> int:
     """Activation rows per tile the tensor-core GEMM uses for M x N on the
     current device (128, 192 or 256; 0 without a usable device)."""
     return int(lib().bsr_gemm_block_m(m, n))
+
+
+# ---------------------------------------------------------------------------
+# integer 4-bit weights with group scales; mixtures of experts
+# ---------------------------------------------------------------------------
+
+
+def _on(t):
+    """A context in which ``t``'s device is the current one (the library
+    launches on the current device, and the default stream is its)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
+
+
+def _beside(t, dtype, shape, name, like):
+    """:func:`_dev` of a tensor that must be on ``like``'s device."""
+    p = _dev(t, dtype, shape, name)
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return p
+
+
+def _w4g_weight(w_q, w_scale, w_zero, lead, n, k, like, name):
+    """The bsr_w4g_weight of codes ``lead + (n, k/2)`` uint8, scales ``lead +
+    (n, k/G)`` bfloat16 or float16, zero points (or None) like the scales,
+    uint8."""
+    torch = _torch()
+    if not isinstance(w_scale, torch.Tensor) or w_scale.dim() != len(lead) + 2:
+        raise ValueError(f"{name} scale must be a tensor of {len(lead) + 2} dimensions")
+    groups = w_scale.shape[-1]
+    if groups == 0 or k % groups or k // groups not in (32, 64, 128):
+        raise ValueError(f"{name}: {groups} scales per row of K={k}: the group must be 32, 64 or 128")
+    if w_scale.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} scale must be bfloat16 or float16, got {w_scale.dtype}")
+    shape = lead + (n, groups)
+    return _W4gWeight(
+        _beside(w_q, torch.uint8, lead + (n, k // 2), f"{name} codes", like).value,
+        _beside(w_scale, w_scale.dtype, shape, f"{name} scale", like).value,
+        None if w_zero is None else _beside(w_zero, torch.uint8, shape, f"{name} zero points", like).value,
+        1 if w_scale.dtype == torch.float16 else 0,
+        k // groups,
+    )
+
+
+def _dims(t, count, name):
+    if t.dim() != count:
+        raise ValueError(f"{name} must have {count} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def w4g_proj(a, w_q, w_scale, w_zero=None, out=None, stream=None):
+    """out [M, N] bfloat16 = a [M, K] (bfloat16) . W^T for an integer 4-bit
+    weight W = (q - zero) * scale: ``w_q`` [N, K/2] uint8 (element 2i in the
+    low nibble of byte i), ``w_scale`` [N, K/G] bfloat16 or float16 with G =
+    32, 64 or 128, ``w_zero`` [N, K/G] uint8 in 0..15 (None: 8)."""
+    torch = _torch()
+    with _on(a):
+        m, k = _dims(a, 2, "a")
+        n = _dims(w_q, 2, "w_q")[0]
+        if out is None:
+            out = _empty((m, n), torch.bfloat16, a)
+        _check(
+            lib().bsr_w4g_proj(
+                _dev(a, torch.bfloat16, (m, k), "a"),
+                _w4g_weight(w_q, w_scale, w_zero, (), n, k, a, "w"),
+                _beside(out, torch.bfloat16, (m, n), "out", a),
+                m,
+                n,
+                k,
+                _stream_ptr(stream),
+            )
+        )
+    return out
+
+
+def w4g_proj_grouped(a, offsets, w_q, w_scale, w_zero=None, rows=None, out=None, stream=None):
+    """:func:`w4g_proj` grouped by expert: output row r with offsets[e] <= r <
+    offsets[e + 1] is ``a[rows[r]]`` (``a[r]`` without ``rows``) times expert
+    e's weight.  ``offsets`` [E + 1] and ``rows`` [R] int32 on the device, as
+    :func:`moe_route` returns them; the weight's tensors have a leading E.
+    Returns out [R, N]; rows at or past offsets[E] are left as they were
+    (uninitialised when ``out`` is not given)."""
+    torch = _torch()
+    with _on(a):
+        a_rows, k = _dims(a, 2, "a")
+        experts, n = _dims(w_q, 3, "w_q")[:2]
+        if rows is None:
+            r = a_rows
+        else:
+            (r,) = _dims(rows, 1, "rows")
+        if out is None:
+            out = _empty((r, n), torch.bfloat16, a)
+        _check(
+            lib().bsr_w4g_proj_grouped(
+                _dev(a, torch.bfloat16, (a_rows, k), "a"),
+                a_rows,
+                _beside(offsets, torch.int32, (experts + 1,), "offsets", a),
+                None if rows is None else _beside(rows, torch.int32, (r,), "rows", a),
+                _w4g_weight(w_q, w_scale, w_zero, (experts,), n, k, a, "w"),
+                _beside(out, torch.bfloat16, (r, n), "out", a),
+                r,
+                experts,
+                n,
+                k,
+                _stream_ptr(stream),
+            )
+        )
+    return out
+
+
+class MoeRoute(NamedTuple):
+    """Result of :func:`moe_route`."""
+
+    ids: Any  # [T, top_k] int32: expert of each slot, -1 where none is left
+    weights: Any  # [T, top_k] float32, 0 where the id is -1
+    offsets: Any  # [E + 1] int32: expert e has the grouped rows offsets[e] .. offsets[e + 1] - 1
+    rows: Any  # [T * top_k] int32: token of each grouped row, -1 past offsets[E]
+    pos: Any  # [T, top_k] int32: grouped row of each pair, -1 where the id is -1
+
+
+def _logits_type(logits):
+    torch = _torch()
+    if logits.dtype == torch.float32:
+        return 0
+    if logits.dtype == torch.bfloat16:
+        return 1
+    raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+
+
+def moe_route_scratch_bytes(tokens: int, experts: int) -> int:
+    return int(lib().bsr_moe_route_scratch_bytes(tokens, experts))
+
+
+def moe_route(logits, top_k: int, renormalize: bool = True, stream=None) -> MoeRoute:
+    """Top-k routing of ``logits`` [T, E] (float32 or bfloat16) and the
+    grouping of the (token, slot) pairs by expert.  Experts with a logit of
+    -inf or NaN are masked; ties go to the lowest index; the weights are a
+    softmax over the chosen experts (``renormalize``) or over all."""
+    torch = _torch()
+    with _on(logits):
+        tokens, experts = _dims(logits, 2, "logits")
+        kind = _logits_type(logits)
+        top_k = int(top_k)
+        if not 1 <= top_k <= experts:
+            raise ValueError(f"top_k must be in 1..{experts}, got {top_k}")
+        need = moe_route_scratch_bytes(tokens, experts)
+        scratch = _empty((need,), torch.uint8, logits) if need else None
+        route = MoeRoute(
+            _empty((tokens, top_k), torch.int32, logits),
+            _empty((tokens, top_k), torch.float32, logits),
+            _empty((experts + 1,), torch.int32, logits),
+            _empty((tokens * top_k,), torch.int32, logits),
+            _empty((tokens, top_k), torch.int32, logits),
+        )
+        _check(
+            lib().bsr_moe_route(
+                _dev(logits, logits.dtype, (tokens, experts), "logits"),
+                kind,
+                tokens,
+                experts,
+                top_k,
+                1 if renormalize else 0,
+                *[t.data_ptr() for t in route],
+                None if scratch is None else scratch.data_ptr(),
+                need,
+                _stream_ptr(stream),
+            )
+        )
+    return route
+
+
+def moe_combine(y, pos, weights, residual=None, out=None, stream=None):
+    """out [T, N] bfloat16 = residual + sum_j weights[:, j] * y[pos[:, j]]
+    (``y`` [R, N] and ``residual`` [T, N] bfloat16; ``pos`` int32 and
+    ``weights`` float32 [T, top_k] as :func:`moe_route` returns them).  A
+    position outside [0, R) is skipped.  ``out`` may be ``residual``."""
+    torch = _torch()
+    with _on(y):
+        r, n = _dims(y, 2, "y")
+        tokens, top_k = _dims(pos, 2, "pos")
+        if out is None:
+            out = _empty((tokens, n), torch.bfloat16, y)
+        _check(
+            lib().bsr_moe_combine(
+                _dev(y, torch.bfloat16, (r, n), "y"),
+                r,
+                _beside(pos, torch.int32, (tokens, top_k), "pos", y),
+                _beside(weights, torch.float32, (tokens, top_k), "weights", y),
+                None if residual is None else _beside(residual, torch.bfloat16, (tokens, n), "residual", y),
+                _beside(out, torch.bfloat16, (tokens, n), "out", y),
+                tokens,
+                top_k,
+                n,
+                _stream_ptr(stream),
+            )
+        )
+    return out
+
+
+def w4g_moe_mlp_scratch_bytes(tokens: int, experts: int, top_k: int, inner: int, k: int) -> int:
+    return int(lib().bsr_w4g_moe_mlp_scratch_bytes(tokens, experts, top_k, inner, k))
+
+
+def w4g_moe_mlp(x, logits, gate, up, down, top_k: int, renormalize: bool = True, residual=None, out=None,
+                scratch=None, stream=None):
+    """The expert MLP: out [T, K] bfloat16 = residual + sum over the top-k
+    experts e of weight_e * down_e(silu(gate_e(x)) * up_e(x)).  ``gate`` and
+    ``up`` are (codes [E, inner, K/2], scale, zero or None), ``down`` the same
+    with [E, K, inner/2].  The same results as :func:`moe_route`,
+    :func:`w4g_proj_grouped`, :func:`silu_mul` and :func:`moe_combine` called
+    one after the other."""
+    torch = _torch()
+    with _on(x):
+        tokens, k = _dims(x, 2, "x")
+        experts = _dims(logits, 2, "logits")[1]
+        inner = _dims(gate[0], 3, "gate codes")[1]
+        if out is None:
+            out = _empty((tokens, k), torch.bfloat16, x)
+        need = w4g_moe_mlp_scratch_bytes(tokens, experts, top_k, inner, k)
+        if scratch is None:
+            scratch = _empty((need,), torch.uint8, x)
+        elif not scratch.is_cuda or scratch.device != x.device:
+            raise ValueError(f"scratch must be on {x.device}")
+        _check(
+            lib().bsr_w4g_moe_mlp(
+                _dev(x, torch.bfloat16, (tokens, k), "x"),
+                _beside(logits, logits.dtype, (tokens, experts), "logits", x),
+                _logits_type(logits),
+                _w4g_weight(*gate, (experts,), inner, k, x, "gate"),
+                _w4g_weight(*up, (experts,), inner, k, x, "up"),
+                _w4g_weight(*down, (experts,), k, inner, x, "down"),
+                None if residual is None else _beside(residual, torch.bfloat16, (tokens, k), "residual", x),
+                _beside(out, torch.bfloat16, (tokens, k), "out", x),
+                tokens,
+                experts,
+                int(top_k),
+                1 if renormalize else 0,
+                inner,
+                k,
+                scratch.data_ptr(),
+                scratch.numel() * scratch.element_size(),
+                _stream_ptr(stream),
+            )
+        )
+    return out

@@ -1,0 +1,44 @@
+// Internal launch interface of the integer 4-bit (group-scale) projections and
+// of the expert router and combine.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace bsr {
+
+// One product over weight rows stacked by expert (dense: one expert, no
+// offsets).  Row r of the output, off[e] <= r < off[e + 1], is row rows[r] of
+// a (r itself when rows is null) times expert e's weight.
+struct W4gArgs {
+  const uint16_t* a;       // [a_rows, K] BF16
+  const int32_t* offsets;  // [experts + 1], or null: one expert with `rows_max` rows
+  const int32_t* rows;     // [rows_max], or null
+  const uint8_t* q;        // [experts * N, K/2], element 2i in the low nibble of byte i
+  const uint16_t* scale;   // [experts * N, K/G] BF16 or FP16
+  const uint8_t* zero;     // [experts * N, K/G], or null: 8
+  uint16_t* out;           // [rows_max, N] BF16
+  long long a_rows, rows_max;
+  int experts, n, k, group;
+  int half_scale;          // scales are FP16
+};
+
+cudaError_t launch_w4g_simple(const W4gArgs& g, cudaStream_t stream);
+
+// Router.  Blocks of route_block_tokens(tokens) tokens; scratch holds one
+// row of `experts` counts per block (none when there is one block).
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTopK = 32;
+long long route_block_tokens(long long tokens);
+size_t route_scratch_bytes(long long tokens, int experts);
+cudaError_t launch_route(const void* logits, bool bf16, long long tokens, int experts, int top_k, bool renorm,
+                         int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, void* scratch,
+                         size_t smem_optin, cudaStream_t stream);
+
+cudaError_t launch_combine(const uint16_t* y, long long y_rows, const int32_t* pos, const float* weights,
+                           const uint16_t* residual, uint16_t* out, long long tokens, int top_k, int n,
+                           cudaStream_t stream, int num_sms);
+
+}  // namespace bsr

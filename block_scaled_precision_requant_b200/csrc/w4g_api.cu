@@ -1,0 +1,310 @@
+// C ABI of the integer 4-bit projections, the expert router and combine, and
+// the expert MLP: argument checks and launches.  Declarations and the
+// contract of every entry point are in include/bsr.h.
+#include <mutex>
+
+#include <cuda_runtime.h>
+
+#include "bsr.h"
+#include "kernels.h"
+#include "w4g.h"
+
+namespace bsr {
+bsr_status library_status_word(int** out);
+bsr_status report(bsr_status st, const char* fmt, ...);
+}  // namespace bsr
+
+namespace {
+
+using bsr::report;
+
+bsr_status ok() { return report(BSR_OK, "%s", ""); }
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+bsr_status cuda_status(cudaError_t e, const char* what) {
+  if (e != cudaSuccess) return report(BSR_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+  return ok();
+}
+
+struct Device {
+  int num_sms = 0;
+  size_t smem_optin = 0;
+  int* status = nullptr;
+};
+Device g_device[64];
+std::mutex g_device_mu;
+
+// The current device's facts (an sm_100 device, else BSR_ENODEV).
+bsr_status device(Device& out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return report(BSR_ENODEV, "cudaGetDevice: %s", cudaGetErrorString(e));
+  if (dev < 0 || dev >= 64) return report(BSR_ENODEV, "device index %d out of range", dev);
+  std::lock_guard<std::mutex> lk(g_device_mu);
+  Device& d = g_device[dev];
+  if (d.num_sms == 0) {
+    int* status = nullptr;
+    const bsr_status st = bsr::library_status_word(&status);
+    if (st != BSR_OK) return st;
+    int sms = 0, smem = 0;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess)
+      return report(BSR_ENODEV, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
+    d.smem_optin = (size_t)smem;
+    d.status = status;
+    d.num_sms = sms;
+  }
+  out = d;
+  return BSR_OK;
+}
+
+bool dim_ok(int64_t x) { return x >= 0 && x <= BSR_MAX_DIM; }
+
+// Everything about a 4-bit weight that does not depend on its pointers.
+bsr_status check_format(const bsr_w4g_weight* w, const char* who, int64_t k) {
+  if (!w) return report(BSR_EINVAL, "%s: null weight", who);
+  if (w->scale_type != BSR_W4G_SCALE_BF16 && w->scale_type != BSR_W4G_SCALE_FP16)
+    return report(BSR_EINVAL, "%s: unknown scale type %d", who, w->scale_type);
+  if (w->group != 32 && w->group != 64 && w->group != 128)
+    return report(BSR_ESHAPE, "%s: group %d is not 32, 64 or 128", who, w->group);
+  if (k <= 0 || k % w->group != 0)
+    return report(BSR_ESHAPE, "%s: K=%lld must be a positive multiple of the group %d", who, (long long)k, w->group);
+  return BSR_OK;
+}
+
+bsr_status check_weight(const bsr_w4g_weight* w, const char* who) {
+  if (!w->q || !w->scale) return report(BSR_EINVAL, "%s: null weight pointer", who);
+  if (!aligned(w->q, 16) || !aligned(w->scale, 2))
+    return report(BSR_EALIGN, "%s: codes must be 16-byte aligned, scales 2-byte aligned", who);
+  return BSR_OK;
+}
+
+bsr::W4gArgs make_args(const uint16_t* a, int64_t a_rows, const int32_t* offsets, const int32_t* rows,
+                       const bsr_w4g_weight* w, uint16_t* out, int64_t r, int64_t experts, int64_t n, int64_t k) {
+  bsr::W4gArgs g = {};
+  g.a = a;
+  g.offsets = offsets;
+  g.rows = rows;
+  g.q = w->q;
+  g.scale = w->scale;
+  g.zero = w->zero;
+  g.out = out;
+  g.a_rows = a_rows;
+  g.rows_max = r;
+  g.experts = (int)experts;
+  g.n = (int)n;
+  g.k = (int)k;
+  g.group = w->group;
+  g.half_scale = w->scale_type == BSR_W4G_SCALE_FP16 ? 1 : 0;
+  return g;
+}
+
+bsr_status run_product(const bsr::W4gArgs& g, void* stream) {
+  Device d;
+  bsr_status st = device(d);
+  if (st != BSR_OK) return st;
+  return cuda_status(bsr::launch_w4g_simple(g, as_stream(stream)), "w4g projection launch");
+}
+
+bsr_status check_route_dims(const char* who, int64_t tokens, int64_t experts, int64_t top_k) {
+  if (tokens < 0 || experts < 1 || experts > bsr::kRouteMaxExperts || top_k < 1 || top_k > experts ||
+      top_k > bsr::kRouteMaxTopK || tokens > BSR_MAX_DIM / top_k)
+    return report(BSR_EINVAL, "%s: tokens=%lld experts=%lld top_k=%lld (1 <= experts <= %d, 1 <= top_k <= "
+                              "min(experts, %d), tokens * top_k < 2^31)",
+                  who, (long long)tokens, (long long)experts, (long long)top_k, bsr::kRouteMaxExperts,
+                  bsr::kRouteMaxTopK);
+  return BSR_OK;
+}
+
+bsr_status check_logits(const char* who, const void* logits, int logits_type, unsigned flags) {
+  if (logits_type != BSR_MOE_LOGITS_F32 && logits_type != BSR_MOE_LOGITS_BF16)
+    return report(BSR_EINVAL, "%s: unknown logits type %d", who, logits_type);
+  if (flags & ~(unsigned)BSR_MOE_RENORMALIZE) return report(BSR_EINVAL, "%s: unknown flags 0x%x", who, flags);
+  if (!logits) return report(BSR_EINVAL, "%s: null logits", who);
+  if (!aligned(logits, logits_type == BSR_MOE_LOGITS_BF16 ? 2 : 4))
+    return report(BSR_EALIGN, "%s: logits must be aligned to their type", who);
+  return BSR_OK;
+}
+
+// Scratch of the expert MLP: the route's results and scratch, then the gate,
+// up, hidden (their SiLU product) and down rows.
+struct MlpLayout {
+  size_t ids, weights, offsets, rows, pos, route, gate, up, hidden, down, total;
+};
+MlpLayout mlp_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner, int64_t k) {
+  const size_t pairs = (size_t)tokens * (size_t)top_k;
+  MlpLayout L;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  L.ids = take(pairs * 4);
+  L.weights = take(pairs * 4);
+  L.offsets = take(((size_t)experts + 1) * 4);
+  L.rows = take(pairs * 4);
+  L.pos = take(pairs * 4);
+  L.route = take(bsr::route_scratch_bytes(tokens, (int)experts));
+  L.gate = take(pairs * (size_t)inner * 2);
+  L.up = take(pairs * (size_t)inner * 2);
+  L.hidden = take(pairs * (size_t)inner * 2);
+  L.down = take(pairs * (size_t)k * 2);
+  L.total = at;
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+bsr_status bsr_w4g_proj(const uint16_t* a, const bsr_w4g_weight* w, uint16_t* out, int64_t m, int64_t n, int64_t k,
+                        void* stream) {
+  bsr_status st = check_format(w, "bsr_w4g_proj", k);
+  if (st != BSR_OK) return st;
+  if (!dim_ok(m) || !dim_ok(n) || !dim_ok(k))
+    return report(BSR_EINVAL, "dimension out of range (m=%lld n=%lld k=%lld)", (long long)m, (long long)n,
+                  (long long)k);
+  if (m == 0 || n == 0) return ok();
+  if (!a || !out) return report(BSR_EINVAL, "bsr_w4g_proj: null pointer");
+  if ((st = check_weight(w, "bsr_w4g_proj")) != BSR_OK) return st;
+  if (!aligned(a, 16) || !aligned(out, 2))
+    return report(BSR_EALIGN, "bsr_w4g_proj: a must be 16-byte aligned, out 2-byte aligned");
+  return run_product(make_args(a, m, nullptr, nullptr, w, out, m, 1, n, k), stream);
+}
+
+bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t* offsets, const int32_t* rows,
+                                const bsr_w4g_weight* w, uint16_t* out, int64_t r, int64_t experts, int64_t n,
+                                int64_t k, void* stream) {
+  bsr_status st = check_format(w, "bsr_w4g_proj_grouped", k);
+  if (st != BSR_OK) return st;
+  if (!dim_ok(a_rows) || !dim_ok(r) || !dim_ok(n) || !dim_ok(k) || experts < 1 || experts > bsr::kRouteMaxExperts ||
+      (n > 0 && experts > BSR_MAX_DIM / n))
+    return report(BSR_EINVAL,
+                  "bsr_w4g_proj_grouped: dimension out of range (a_rows=%lld r=%lld experts=%lld n=%lld k=%lld; "
+                  "experts <= %d, experts * n < 2^31)",
+                  (long long)a_rows, (long long)r, (long long)experts, (long long)n, (long long)k,
+                  bsr::kRouteMaxExperts);
+  if (r == 0 || n == 0) return ok();
+  if (!a || !offsets || !out) return report(BSR_EINVAL, "bsr_w4g_proj_grouped: null pointer");
+  if (!rows && a_rows < r)
+    return report(BSR_EINVAL, "bsr_w4g_proj_grouped: a has %lld rows, %lld are needed without a row index",
+                  (long long)a_rows, (long long)r);
+  if ((st = check_weight(w, "bsr_w4g_proj_grouped")) != BSR_OK) return st;
+  if (!aligned(a, 16) || !aligned(out, 2) || !aligned(offsets, 4) || !aligned(rows, 4))
+    return report(BSR_EALIGN, "bsr_w4g_proj_grouped: a must be 16-byte aligned, offsets and rows 4-byte, out 2-byte");
+  return run_product(make_args(a, a_rows, offsets, rows, w, out, r, experts, n, k), stream);
+}
+
+size_t bsr_moe_route_scratch_bytes(int64_t tokens, int64_t experts) {
+  if (tokens <= 0 || experts < 1 || experts > bsr::kRouteMaxExperts) return 0;
+  return bsr::route_scratch_bytes(tokens, (int)experts);
+}
+
+bsr_status bsr_moe_route(const void* logits, int logits_type, int64_t tokens, int64_t experts, int64_t top_k,
+                         unsigned flags, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos,
+                         void* scratch, size_t scratch_bytes, void* stream) {
+  bsr_status st = check_route_dims("bsr_moe_route", tokens, experts, top_k);
+  if (st != BSR_OK) return st;
+  if (tokens > 0) {
+    if ((st = check_logits("bsr_moe_route", logits, logits_type, flags)) != BSR_OK) return st;
+    if (!ids || !weights || !rows || !pos) return report(BSR_EINVAL, "bsr_moe_route: null pointer");
+  }
+  if (!offsets) return report(BSR_EINVAL, "bsr_moe_route: null offsets");
+  if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(pos, 4))
+    return report(BSR_EALIGN, "bsr_moe_route: outputs must be 4-byte aligned");
+  const size_t need = bsr_moe_route_scratch_bytes(tokens, experts);
+  if (need && (!scratch || scratch_bytes < need))
+    return report(BSR_ESCRATCH, "scratch of %zu bytes needed, %zu given", need, scratch ? scratch_bytes : (size_t)0);
+  if (need && !aligned(scratch, 4)) return report(BSR_EALIGN, "bsr_moe_route: scratch must be 4-byte aligned");
+  Device d;
+  if ((st = device(d)) != BSR_OK) return st;
+  return cuda_status(bsr::launch_route(logits, logits_type == BSR_MOE_LOGITS_BF16, tokens, (int)experts, (int)top_k,
+                                       (flags & BSR_MOE_RENORMALIZE) != 0, ids, weights, offsets, rows, pos, scratch,
+                                       d.smem_optin, as_stream(stream)),
+                     "route launch");
+}
+
+bsr_status bsr_moe_combine(const uint16_t* y, int64_t y_rows, const int32_t* pos, const float* weights,
+                           const uint16_t* residual, uint16_t* out, int64_t tokens, int64_t top_k, int64_t n,
+                           void* stream) {
+  if (!dim_ok(y_rows) || !dim_ok(n) || tokens < 0 || top_k < 1 || top_k > bsr::kRouteMaxTopK ||
+      tokens > BSR_MAX_DIM / top_k)
+    return report(BSR_EINVAL, "bsr_moe_combine: dimension out of range (y_rows=%lld tokens=%lld top_k=%lld n=%lld)",
+                  (long long)y_rows, (long long)tokens, (long long)top_k, (long long)n);
+  if (tokens == 0 || n == 0) return ok();
+  if ((!y && y_rows > 0) || !pos || !weights || !out) return report(BSR_EINVAL, "bsr_moe_combine: null pointer");
+  if (!aligned(y, 2) || !aligned(pos, 4) || !aligned(weights, 4) || !aligned(residual, 2) || !aligned(out, 2))
+    return report(BSR_EALIGN, "bsr_moe_combine: pointers must be aligned to their types");
+  Device d;
+  bsr_status st = device(d);
+  if (st != BSR_OK) return st;
+  return cuda_status(bsr::launch_combine(y, y_rows, pos, weights, residual, out, tokens, (int)top_k, (int)n,
+                                         as_stream(stream), d.num_sms),
+                     "combine launch");
+}
+
+size_t bsr_w4g_moe_mlp_scratch_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner, int64_t k) {
+  if (tokens <= 0 || experts < 1 || experts > bsr::kRouteMaxExperts || top_k < 1 || top_k > experts ||
+      top_k > bsr::kRouteMaxTopK || tokens > BSR_MAX_DIM / top_k || !dim_ok(inner) || !dim_ok(k) || inner == 0 ||
+      k == 0)
+    return 0;
+  return mlp_layout(tokens, experts, top_k, inner, k).total;
+}
+
+bsr_status bsr_w4g_moe_mlp(const uint16_t* x, const void* logits, int logits_type, const bsr_w4g_weight* gate,
+                           const bsr_w4g_weight* up, const bsr_w4g_weight* down, const uint16_t* residual,
+                           uint16_t* out, int64_t tokens, int64_t experts, int64_t top_k, unsigned flags,
+                           int64_t inner, int64_t k, void* scratch, size_t scratch_bytes, void* stream) {
+  static const char* const who = "bsr_w4g_moe_mlp";
+  bsr_status st = check_route_dims(who, tokens, experts, top_k);
+  if (st != BSR_OK) return st;
+  if ((st = check_format(gate, who, k)) != BSR_OK || (st = check_format(up, who, k)) != BSR_OK ||
+      (st = check_format(down, who, inner)) != BSR_OK)
+    return st;
+  if (!dim_ok(inner) || !dim_ok(k) || experts > BSR_MAX_DIM / inner || experts > BSR_MAX_DIM / k)
+    return report(BSR_EINVAL, "%s: dimension out of range (inner=%lld k=%lld; experts times each < 2^31)", who,
+                  (long long)inner, (long long)k);
+  if (tokens == 0) return ok();
+  if ((st = check_logits(who, logits, logits_type, flags)) != BSR_OK) return st;
+  if (!x || !out) return report(BSR_EINVAL, "%s: null pointer", who);
+  if ((st = check_weight(gate, who)) != BSR_OK || (st = check_weight(up, who)) != BSR_OK ||
+      (st = check_weight(down, who)) != BSR_OK)
+    return st;
+  if (!aligned(x, 16) || !aligned(residual, 2) || !aligned(out, 2))
+    return report(BSR_EALIGN, "%s: x must be 16-byte aligned, residual and out 2-byte aligned", who);
+  const MlpLayout L = mlp_layout(tokens, experts, top_k, inner, k);
+  if (!scratch || scratch_bytes < L.total)
+    return report(BSR_ESCRATCH, "scratch of %zu bytes needed, %zu given", L.total, scratch ? scratch_bytes : (size_t)0);
+  if (!aligned(scratch, 256)) return report(BSR_EALIGN, "scratch must be 256-byte aligned");
+  Device d;
+  if ((st = device(d)) != BSR_OK) return st;
+  const int64_t pairs = tokens * top_k;
+  uint8_t* s = static_cast<uint8_t*>(scratch);
+  int32_t* ids = reinterpret_cast<int32_t*>(s + L.ids);
+  float* weights = reinterpret_cast<float*>(s + L.weights);
+  int32_t* offsets = reinterpret_cast<int32_t*>(s + L.offsets);
+  int32_t* rows = reinterpret_cast<int32_t*>(s + L.rows);
+  int32_t* pos = reinterpret_cast<int32_t*>(s + L.pos);
+  uint16_t* g = reinterpret_cast<uint16_t*>(s + L.gate);
+  uint16_t* u = reinterpret_cast<uint16_t*>(s + L.up);
+  uint16_t* h = reinterpret_cast<uint16_t*>(s + L.hidden);
+  uint16_t* y = reinterpret_cast<uint16_t*>(s + L.down);
+  if ((st = bsr_moe_route(logits, logits_type, tokens, experts, top_k, flags, ids, weights, offsets, rows, pos,
+                          s + L.route, L.gate - L.route, stream)) != BSR_OK)
+    return st;
+  if ((st = run_product(make_args(x, tokens, offsets, rows, gate, g, pairs, experts, inner, k), stream)) != BSR_OK)
+    return st;
+  if ((st = run_product(make_args(x, tokens, offsets, rows, up, u, pairs, experts, inner, k), stream)) != BSR_OK)
+    return st;
+  if ((st = cuda_status(bsr::launch_silu_mul(g, u, h, (int)pairs, (int)inner, as_stream(stream), d.num_sms),
+                        "silu_mul launch")) != BSR_OK)
+    return st;
+  if ((st = run_product(make_args(h, pairs, offsets, nullptr, down, y, pairs, experts, k, inner), stream)) != BSR_OK)
+    return st;
+  return bsr_moe_combine(y, pairs, pos, weights, residual, out, tokens, top_k, k, stream);
+}
+
+}  // extern "C"

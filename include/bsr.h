@@ -416,6 +416,112 @@ bsr_status bsr_proj_silu(const uint16_t* gate, const uint16_t* up, const int8_t*
                          uint16_t* out, int64_t m, int64_t n, int64_t k, void* scratch, size_t scratch_bytes,
                          void* stream);
 
+/*
+ * Integer 4-bit weights with group scales, and the operators of a mixture of
+ * experts over them.  No counterpart on the launcher pages: these are this
+ * library's additions.
+ *
+ * A weight [N, K] holds unsigned codes q in 0..15, two per byte (element 2i
+ * in the low nibble of byte i), and per group of G consecutive elements of a
+ * row one scale s (BF16 or FP16) and, optionally, one zero point z (one byte,
+ * 0..15; 8 where there are none):
+ *   W[n, k] = (q[n, k] - z[n, k / G]) * s[n, k / G],   G in {32, 64, 128}.
+ * The experts' weights of one projection are stacked: codes [E, N, K/2],
+ * scales [E, N, K/G], zero points [E, N, K/G].  Zero points above 15 are
+ * outside the contract (results unspecified).
+ */
+#define BSR_W4G_SCALE_BF16 0
+#define BSR_W4G_SCALE_FP16 1
+typedef struct bsr_w4g_weight {
+  const uint8_t* q;      /* device, 16-byte aligned */
+  const uint16_t* scale; /* device, 2-byte aligned */
+  const uint8_t* zero;   /* device, or NULL: every zero point is 8 */
+  int scale_type;        /* BSR_W4G_SCALE_BF16 or BSR_W4G_SCALE_FP16 */
+  int group;             /* G */
+} bsr_w4g_weight;
+
+/* Bounds of the expert operators. */
+#define BSR_MOE_MAX_EXPERTS 1024
+#define BSR_MOE_MAX_TOP_K 32
+
+/*
+ * bsr_w4g_proj -- out[M, N] = A[M, K] . W[N, K]^T for BF16 activations and an
+ * integer 4-bit weight, on the weight as stored:
+ *   out[m, n] = bf16( sum_g s[n, g] * sum_{k in g} a[m, k] * (q[n, k] - z[n, g]) ).
+ * The products a * (q - z) are exact; the sums are float32.  K % G == 0
+ * (BSR_ESHAPE); a 16-byte aligned, out 2-byte aligned.
+ */
+bsr_status bsr_w4g_proj(const uint16_t* a, const bsr_w4g_weight* w, uint16_t* out, int64_t m, int64_t n, int64_t k,
+                        void* stream);
+
+/*
+ * bsr_w4g_proj_grouped -- the same product grouped by expert, with ragged
+ * group sizes: output row r, offsets[e] <= r < offsets[e + 1], is row rows[r]
+ * of a [a_rows, K] (row r itself when rows is NULL; then a_rows >= R) times
+ * expert e's weight.  offsets [E + 1] and rows [R] are device arrays (as
+ * bsr_moe_route writes them); the host never reads them.  offsets[0] is taken
+ * as 0, each later offset is clamped to [the one before, R]; a row index
+ * outside [0, a_rows) stands for a row of zeros.  Rows of out at or past
+ * offsets[E] are left as they were.  1 <= E <= BSR_MOE_MAX_EXPERTS, E * N
+ * below 2^31; shapes and alignment as bsr_w4g_proj.
+ */
+bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t* offsets, const int32_t* rows,
+                                const bsr_w4g_weight* w, uint16_t* out, int64_t r, int64_t experts, int64_t n,
+                                int64_t k, void* stream);
+
+/*
+ * bsr_moe_route -- top-k routing and the grouping of its (token, slot) pairs
+ * by expert.  logits [T, E] float32 or BF16.  An expert whose logit is -inf
+ * or NaN is masked: never chosen, probability 0.  Per token the top_k
+ * unmasked experts by logit, largest first, ties to the lowest index:
+ *   ids     [T, top_k]   expert, or -1 where no unmasked expert is left
+ *   weights [T, top_k]   softmax over all unmasked experts, or over the
+ *                        chosen ones with BSR_MOE_RENORMALIZE; 0 where id is -1
+ *   offsets [E + 1]      the groups: pairs of expert e, in (token, slot)
+ *                        order, are rows offsets[e] .. offsets[e + 1] - 1
+ *   rows    [T * top_k]  token of each grouped row; -1 past offsets[E]
+ *   pos     [T, top_k]   grouped row of each pair, or -1 where id is -1
+ * (A padded batch gives its padding tokens rows of -inf.)  T * top_k < 2^31,
+ * top_k <= min(E, BSR_MOE_MAX_TOP_K), E <= BSR_MOE_MAX_EXPERTS.  T == 0
+ * writes offsets only.  Scratch (device, 4-byte aligned) of
+ * bsr_moe_route_scratch_bytes(T, E), which may be 0.  Results do not depend
+ * on scheduling.
+ */
+#define BSR_MOE_LOGITS_F32 0
+#define BSR_MOE_LOGITS_BF16 1
+#define BSR_MOE_RENORMALIZE 1u
+size_t bsr_moe_route_scratch_bytes(int64_t tokens, int64_t experts);
+bsr_status bsr_moe_route(const void* logits, int logits_type, int64_t tokens, int64_t experts, int64_t top_k,
+                         unsigned flags, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos,
+                         void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * bsr_moe_combine -- the weighted sum of each token's expert rows:
+ *   out[t, :] = bf16( residual[t, :] + sum_j weights[t, j] * y[pos[t, j], :] )
+ * in float32, residual first, then slots in order.  y [y_rows, N] BF16, pos
+ * and weights [T, top_k], residual [T, N] BF16 or NULL (may be out itself).
+ * A position outside [0, y_rows) is skipped whatever its weight.
+ */
+bsr_status bsr_moe_combine(const uint16_t* y, int64_t y_rows, const int32_t* pos, const float* weights,
+                           const uint16_t* residual, uint16_t* out, int64_t tokens, int64_t top_k, int64_t n,
+                           void* stream);
+
+/*
+ * bsr_w4g_moe_mlp -- the expert MLP: bsr_moe_route of the logits, the gate
+ * and up projections of each pair's token (weights [E, inner, K]),
+ * bsr_silu_mul, the down projection (weight [E, K, inner]) and
+ * bsr_moe_combine.  The same results as those calls made one after the
+ * other.  x, residual (or NULL) and out are [T, K] BF16; out may be residual,
+ * not x.  The three weights need not share a group or scale type.  Scratch
+ * (device, 256-byte aligned) of bsr_w4g_moe_mlp_scratch_bytes bytes (0 for
+ * invalid sizes).  Every check that can fail comes before the first launch.
+ */
+size_t bsr_w4g_moe_mlp_scratch_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner, int64_t k);
+bsr_status bsr_w4g_moe_mlp(const uint16_t* x, const void* logits, int logits_type, const bsr_w4g_weight* gate,
+                           const bsr_w4g_weight* up, const bsr_w4g_weight* down, const uint16_t* residual,
+                           uint16_t* out, int64_t tokens, int64_t experts, int64_t top_k, unsigned flags,
+                           int64_t inner, int64_t k, void* scratch, size_t scratch_bytes, void* stream);
+
 /* Size of the device array bsr_proj_noalloc uses as its scratch: 16 MiB,
  * enough for M*K + (K/32)*round_up(M,4)*4 <= 16 MiB (e.g. M=2048, K=4096 or
  * M=3584, K=4096; not M=4095, K=8192). */

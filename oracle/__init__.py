@@ -415,3 +415,73 @@ def w4a4_proj(a_bits, w_packed, w_e4m3, scale2_w, k: int) -> np.ndarray:
     vw = _nvfp4_unscaled(w_packed, w_e4m3, k)
     acc = (va @ vw.T) * (as2.astype(np.float64)[:, None] * float(np.float32(scale2_w)))
     return bf16_rne(acc.astype(np.float32))
+
+
+# ---------------------------------------------------------------------------
+# Integer 4-bit weights with group scales; mixtures of experts
+# ---------------------------------------------------------------------------
+
+
+def w4g_dequant(codes: np.ndarray, scale: np.ndarray, zero: np.ndarray | None) -> np.ndarray:
+    """float64 weight (q - zero) * scale: codes [N, K/2] uint8 (element 2i in
+    the low nibble of byte i), scale [N, K/G] of any float type, zero [N, K/G]
+    or None (8).  Exact: a product of a 5-bit integer and a 16-bit float."""
+    n, half = codes.shape
+    q = np.empty((n, 2 * half), dtype=np.float64)
+    q[:, 0::2] = codes & 15
+    q[:, 1::2] = codes >> 4
+    g = 2 * half // scale.shape[1]
+    z = np.full(scale.shape, 8.0) if zero is None else zero.astype(np.float64)
+    return (q - np.repeat(z, g, axis=1)) * np.repeat(scale.astype(np.float64), g, axis=1)
+
+
+def w4g_proj(a: np.ndarray, codes: np.ndarray, scale: np.ndarray, zero: np.ndarray | None):
+    """(a . W^T, sum of |a| |w|) in float64 for float64 activations [M, K]."""
+    w = w4g_dequant(codes, scale, zero)
+    return a @ w.T, np.abs(a) @ np.abs(w).T
+
+
+def moe_route(logits: np.ndarray, top_k: int, renormalize: bool = True):
+    """(ids, weights float64, offsets, rows, pos) of bsr_moe_route, written as
+    loops over tokens and pairs."""
+    t, e = logits.shape
+    x = logits.astype(np.float64)
+    masked = ~(x > -np.inf)  # -inf or NaN
+    ids = np.full((t, top_k), -1, dtype=np.int32)
+    weights = np.zeros((t, top_k))
+    for i in range(t):
+        left = [j for j in range(e) if not masked[i, j]]
+        order = sorted(left, key=lambda j: (-x[i, j], j))[:top_k]
+        if not order:
+            continue
+        top = x[i, order[0]]
+        p = {j: 1.0 if x[i, j] == top else np.exp(x[i, j] - top) for j in left}
+        total = sum(p[j] for j in (order if renormalize else left))
+        for s, j in enumerate(order):
+            ids[i, s] = j
+            weights[i, s] = p[j] / total
+    offsets = np.zeros(e + 1, dtype=np.int32)
+    rows = np.full(t * top_k, -1, dtype=np.int32)
+    pos = np.full((t, top_k), -1, dtype=np.int32)
+    r = 0
+    for j in range(e):
+        for i, s in zip(*np.nonzero(ids == j)):
+            rows[r] = i
+            pos[i, s] = r
+            r += 1
+        offsets[j + 1] = r
+    return ids, weights, offsets, rows, pos
+
+
+def moe_combine(y: np.ndarray, pos: np.ndarray, weights: np.ndarray, residual: np.ndarray | None):
+    """(sum, sum of magnitudes) in float64; positions outside y are skipped."""
+    t, k = pos.shape
+    out = np.zeros((t, y.shape[1])) if residual is None else residual.astype(np.float64)
+    mag = np.abs(out)
+    for i in range(t):
+        for s in range(k):
+            if 0 <= pos[i, s] < y.shape[0]:
+                term = float(weights[i, s]) * y[pos[i, s]].astype(np.float64)
+                out[i] = out[i] + term
+                mag[i] = mag[i] + np.abs(term)
+    return out, mag

@@ -1,0 +1,134 @@
+"""Argument checks of the integer 4-bit and expert entry points (no GPU
+needed: each returns before it touches a device or a pointer)."""
+import ctypes
+
+import pytest
+import torch
+
+import block_scaled_precision_requant_b200 as bsr
+from block_scaled_precision_requant_b200 import build
+
+P = ctypes.c_void_p
+OK, EINVAL, EALIGN, ESHAPE, ESCRATCH = 0, 1, 2, 3, 4
+A = P(256)
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return bsr.lib()
+
+
+def weight(q=256, scale=256, zero=None, kind=0, group=64):
+    return ctypes.byref(bsr._W4gWeight(q, scale, zero, kind, group))
+
+
+def test_constants_match_the_header():
+    import os
+    import re
+
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "bsr.h")).read()
+    d = dict(re.findall(r"^#define (BSR_(?:W4G|MOE)_\w+) (\d+)u?$", src, flags=re.M))
+    assert d == {"BSR_W4G_SCALE_BF16": "0", "BSR_W4G_SCALE_FP16": "1", "BSR_MOE_MAX_EXPERTS": "1024",
+                 "BSR_MOE_MAX_TOP_K": "32", "BSR_MOE_LOGITS_F32": "0", "BSR_MOE_LOGITS_BF16": "1",
+                 "BSR_MOE_RENORMALIZE": "1"}
+    fields = re.search(r"typedef struct bsr_w4g_weight \{(.*?)\}", src, flags=re.S).group(1)
+    assert re.findall(r"(\w+);", fields) == [n for n, _ in bsr._W4gWeight._fields_]
+
+
+def test_proj(L):
+    assert L.bsr_w4g_proj(A, None, A, 1, 8, 64, None) == EINVAL
+    assert L.bsr_w4g_proj(A, weight(kind=2), A, 1, 8, 64, None) == EINVAL
+    assert L.bsr_w4g_proj(A, weight(group=16), A, 1, 8, 64, None) == ESHAPE
+    assert L.bsr_w4g_proj(A, weight(), A, 1, 8, 96, None) == ESHAPE and "group 64" in bsr.last_error()
+    assert L.bsr_w4g_proj(A, weight(), A, 1, 8, 0, None) == ESHAPE
+    assert L.bsr_w4g_proj(A, weight(), A, -1, 8, 64, None) == EINVAL
+    assert L.bsr_w4g_proj(A, weight(), A, 1, 2 ** 31, 64, None) == EINVAL
+    assert L.bsr_w4g_proj(None, weight(), A, 1, 8, 64, None) == EINVAL
+    assert L.bsr_w4g_proj(A, weight(q=None), A, 1, 8, 64, None) == EINVAL
+    assert L.bsr_w4g_proj(A, weight(q=264), A, 1, 8, 64, None) == EALIGN
+    assert L.bsr_w4g_proj(A, weight(scale=257), A, 1, 8, 64, None) == EALIGN
+    assert L.bsr_w4g_proj(P(264), weight(), A, 1, 8, 64, None) == EALIGN
+    assert L.bsr_w4g_proj(A, weight(), P(257), 1, 8, 64, None) == EALIGN
+    assert L.bsr_w4g_proj(None, weight(None, None), None, 0, 8, 64, None) == OK
+    assert L.bsr_w4g_proj(None, weight(None, None), None, 8, 0, 64, None) == OK
+
+
+def test_proj_grouped(L):
+    def call(a=A, a_rows=4, off=A, rows=A, w=None, out=A, r=4, e=2, n=8, k=64):
+        return L.bsr_w4g_proj_grouped(a, a_rows, off, rows, w or weight(), out, r, e, n, k, None)
+
+    assert call(e=0) == EINVAL and call(e=1025) == EINVAL and call(n=2 ** 30, e=2) == EINVAL
+    assert call(r=-1) == EINVAL and call(a_rows=-1) == EINVAL
+    assert call(off=None) == EINVAL and call(a=None) == EINVAL and call(out=None) == EINVAL
+    assert call(rows=None, a_rows=3) == EINVAL and "row index" in bsr.last_error()
+    assert call(off=P(258)) == EALIGN and call(rows=P(258)) == EALIGN and call(a=P(264)) == EALIGN
+    assert call(w=weight(q=8)) == EALIGN and call(k=32) == ESHAPE
+    assert call(a=None, off=None, rows=None, out=None, r=0) == OK
+
+
+def test_route(L):
+    def call(logits=A, kind=0, t=4, e=8, k=2, flags=0, out=(A, A, A, A, A), scratch=None, nbytes=0):
+        return L.bsr_moe_route(logits, kind, t, e, k, flags, *out, scratch, nbytes, None)
+
+    assert call(e=0) == EINVAL and call(e=1025) == EINVAL and call(k=0) == EINVAL and call(k=9) == EINVAL
+    assert call(e=64, k=33) == EINVAL and call(t=-1) == EINVAL and call(t=2 ** 30, k=2) == EINVAL
+    assert call(kind=2) == EINVAL and call(flags=2) == EINVAL and call(logits=None) == EINVAL
+    assert call(logits=P(258)) == EALIGN and call(logits=P(257), kind=1) == EALIGN
+    for i in range(5):
+        assert call(out=tuple(None if j == i else A for j in range(5))) == EINVAL
+        assert call(out=tuple(P(258) if j == i else A for j in range(5))) == EALIGN
+    assert L.bsr_moe_route_scratch_bytes(128, 8) == 0
+    need = L.bsr_moe_route_scratch_bytes(129, 8)
+    assert need == 2 * 8 * 4 and L.bsr_moe_route_scratch_bytes(10 ** 6, 64) <= 128 * 64 * 4
+    assert call(t=129) == ESCRATCH and call(t=129, scratch=A, nbytes=need - 1) == ESCRATCH
+    assert call(t=129, scratch=P(258), nbytes=need) == EALIGN
+
+
+def test_combine(L):
+    def call(y=A, rows=8, pos=A, w=A, res=None, out=A, t=4, k=2, n=8):
+        return L.bsr_moe_combine(y, rows, pos, w, res, out, t, k, n, None)
+
+    assert call(t=-1) == EINVAL and call(k=0) == EINVAL and call(k=33) == EINVAL and call(n=-1) == EINVAL
+    assert call(y=None) == EINVAL and call(pos=None) == EINVAL and call(w=None) == EINVAL and call(out=None) == EINVAL
+    assert call(y=P(257)) == EALIGN and call(pos=P(258)) == EALIGN and call(res=P(257)) == EALIGN
+    assert call(None, 0, None, None, None, None, 0) == OK and call(None, 0, None, None, None, None, n=0) == OK
+
+
+def test_mlp(L):
+    need = L.bsr_w4g_moe_mlp_scratch_bytes(4, 8, 2, 64, 128)
+    assert need > 0 and need % 256 == 0
+    for bad in ((0, 8, 2, 64, 128), (4, 0, 2, 64, 128), (4, 8, 9, 64, 128), (4, 8, 2, 0, 128), (4, 8, 2, 64, 0)):
+        assert L.bsr_w4g_moe_mlp_scratch_bytes(*bad) == 0
+
+    def call(x=A, logits=A, kind=0, gate=None, up=None, down=None, res=None, out=A, t=4, e=8, k=2, flags=1, inner=64,
+             hidden=128, scratch=A, nbytes=need):
+        return L.bsr_w4g_moe_mlp(x, logits, kind, gate or weight(), up or weight(), down or weight(), res, out, t, e,
+                                 k, flags, inner, hidden, scratch, nbytes, None)
+
+    assert call(k=9) == EINVAL and call(flags=4) == EINVAL and call(kind=3) == EINVAL and call(x=None) == EINVAL
+    assert call(inner=96) == ESHAPE and call(hidden=96) == ESHAPE and call(down=weight(group=48)) == ESHAPE
+    assert call(up=weight(q=None)) == EINVAL and call(down=weight(q=8)) == EALIGN and call(x=P(258)) == EALIGN
+    assert call(scratch=None) == ESCRATCH and call(nbytes=need - 1) == ESCRATCH and call(scratch=P(128)) == EALIGN
+    assert call(x=None, logits=None, out=None, t=0) == OK
+
+
+def test_binding_refuses_before_the_library():
+    a = torch.zeros(2, 64, dtype=torch.bfloat16)
+    q, s = torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        bsr.w4g_proj(a, q, s)
+    with pytest.raises(ValueError, match="dimensions"):
+        bsr.w4g_proj(a[0], q, s)
+    with pytest.raises(ValueError, match="dimensions"):
+        bsr.w4g_proj_grouped(a, torch.zeros(2, dtype=torch.int32), q, s)
+    with pytest.raises(TypeError):
+        bsr.w4g_proj([1.0], q, s)
+    with pytest.raises(ValueError, match="top_k"):
+        bsr.moe_route(torch.zeros(2, 4), 5)
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        bsr.moe_route(torch.zeros(2, 4, dtype=torch.float64), 2)
+    for groups, kind, error in ((3, torch.bfloat16, ValueError), (1, torch.float32, TypeError),
+                                (4, torch.bfloat16, ValueError), (0, torch.bfloat16, ValueError)):
+        with pytest.raises(error):
+            bsr._w4g_weight(q, torch.zeros(8, groups, dtype=kind), None, (), 8, 64, a, "w")
