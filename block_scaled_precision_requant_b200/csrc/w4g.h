@@ -25,6 +25,17 @@ struct W4gArgs {
   int half_scale;          // scales are FP16
 };
 
+// Few rows per expert: warp-level tensor instructions fed by a streamed weight.
+// Items of rb weight rows x 8 nt activation rows, ks warps along K; the codes'
+// tensor map has boxes of rb rows x 128 bytes with the 128-byte swizzle.
+struct W4gGemvPlan {
+  int rb, rt, nt, ks, slots, nblk, chunks, grid;
+  size_t smem;
+};
+W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms);
+cudaError_t launch_w4g_gemv(const CUtensorMap& tm_q, const W4gArgs& g, const W4gGemvPlan& p, int* status,
+                            cudaStream_t stream);
+
 cudaError_t launch_w4g_simple(const W4gArgs& g, cudaStream_t stream);
 
 // Router.  Blocks of route_block_tokens(tokens) tokens; scratch holds one

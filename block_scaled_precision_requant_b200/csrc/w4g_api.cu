@@ -101,10 +101,53 @@ bsr::W4gArgs make_args(const uint16_t* a, int64_t a_rows, const int32_t* offsets
   return g;
 }
 
+// cuTensorMapEncodeTiled through the runtime's driver entry point, so the
+// library does not link libcuda directly.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+bsr_status encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+                     uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw,
+                     const char* what) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return report(BSR_ECUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {pitch_bytes};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return report(BSR_ECUDA, "cuTensorMapEncodeTiled(%s) failed: %d", what, (int)r);
+  return BSR_OK;
+}
+
 bsr_status run_product(const bsr::W4gArgs& g, void* stream) {
   Device d;
   bsr_status st = device(d);
   if (st != BSR_OK) return st;
+  if (g.rows_max <= 16LL * g.experts && g.rows_max <= 4096) {
+    const bsr::W4gGemvPlan p = bsr::w4g_gemv_plan(g, d.num_sms);
+    CUtensorMap tm;
+    if ((st = encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, (uint64_t)g.k / 2, (uint64_t)g.experts * g.n,
+                        (uint64_t)g.k / 2, 128, (uint32_t)p.rb, CU_TENSOR_MAP_SWIZZLE_128B, "w4g codes")) != BSR_OK)
+      return st;
+    return cuda_status(bsr::launch_w4g_gemv(tm, g, p, d.status, as_stream(stream)), "w4g projection launch");
+  }
   return cuda_status(bsr::launch_w4g_simple(g, as_stream(stream)), "w4g projection launch");
 }
 
