@@ -26,10 +26,11 @@ struct W4gArgs {
 };
 
 // Few rows per expert: warp-level tensor instructions fed by a streamed weight.
-// Items of rb weight rows x 8 nt activation rows, ks warps along K; the codes'
-// tensor map has boxes of rb rows x 128 bytes with the 128-byte swizzle.
+// Items of rt tiles of tr (<= 16) weight rows x 8 nt activation rows, ks warps
+// along K; the codes' tensor map has boxes of tr rows x 128 bytes with the
+// 128-byte swizzle.
 struct W4gGemvPlan {
-  int rb, rt, nt, ks, slots, nblk, chunks, grid;
+  int tr, rt, nt, ks, slots, nblk, chunks, grid;
   size_t smem;
 };
 W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms);

@@ -144,7 +144,7 @@ bsr_status run_product(const bsr::W4gArgs& g, void* stream) {
     const bsr::W4gGemvPlan p = bsr::w4g_gemv_plan(g, d.num_sms);
     CUtensorMap tm;
     if ((st = encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, (uint64_t)g.k / 2, (uint64_t)g.experts * g.n,
-                        (uint64_t)g.k / 2, 128, (uint32_t)p.rb, CU_TENSOR_MAP_SWIZZLE_128B, "w4g codes")) != BSR_OK)
+                        (uint64_t)g.k / 2, 128, (uint32_t)p.tr, CU_TENSOR_MAP_SWIZZLE_128B, "w4g codes")) != BSR_OK)
       return st;
     return cuda_status(bsr::launch_w4g_gemv(tm, g, p, d.status, as_stream(stream)), "w4g projection launch");
   }

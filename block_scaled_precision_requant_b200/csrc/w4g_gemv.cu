@@ -42,19 +42,24 @@ constexpr int kWarps = 8;
 constexpr int kChunk = 256;       // elements of K per chunk
 constexpr int kChunkBytes = 128;  // of codes
 
+constexpr int kSlotBytes = 16 * kChunkBytes;
+
 struct GemvCfg {
-  int rb, ks, slots, nblk, chunks;
+  int tr, rt, ks, slots, nblk, chunks;
+  int vec;  // scales (and zero points) of a lane may be read as one vector
 };
 
 struct GemvSmem {
-  uint32_t slot_bytes, red, bars, off, pre, abort_flag, total;
+  uint32_t meta, red, bars, off, pre, abort_flag, total;
 };
 
-__host__ __device__ inline GemvSmem gemv_smem(int rt, int nt, int slots, int experts) {
+// Per-warp ring of tile slots, per-warp scales of one tile and segment, the
+// warps' sums of an item, barriers, offsets and items before each expert.
+__host__ __device__ inline GemvSmem gemv_smem(int rt, int nt, int group, int slots, int experts) {
   GemvSmem L;
-  L.slot_bytes = (uint32_t)rt * 16u * kChunkBytes;
-  L.red = kWarps * (uint32_t)slots * L.slot_bytes;
-  L.bars = L.red + kWarps * (uint32_t)(rt * 16 + 1) * (uint32_t)(nt * 8) * 4u;
+  L.meta = kWarps * (uint32_t)slots * kSlotBytes;
+  L.red = L.meta + kWarps * (uint32_t)(kChunk / group / nt) * 8u * 16u;
+  L.bars = L.red + kWarps * (uint32_t)(rt * 16) * (uint32_t)(nt * 8) * 4u;
   L.off = L.bars + kWarps * (uint32_t)slots * 8u;
   L.pre = L.off + (uint32_t)(experts + 1) * 4u;
   L.abort_flag = L.pre + (uint32_t)(experts + 1) * 4u;
@@ -66,17 +71,30 @@ __device__ __forceinline__ float scale_f32(uint16_t s, int half) {
   return half ? __half2float(__ushort_as_half(s)) : __uint_as_float((uint32_t)s << 16);
 }
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
 
-// 8 codes of a word -> four BF16 pairs (q_j - z, q_{j+4} - z); zc = the pair
-// 128 + z.
+// 8 codes of a word -> four BF16 pairs ((q_j - z) / 64, (q_{j+4} - z) / 64),
+// exact; zc = the pair -z / 64.  Bits below 256 read as BF16 are that integer
+// times 2^-133 (subnormal below 128, the first normal binade above), so a
+// nibble in bits 0-3 or 4-7 of a half needs no shift and no exponent: the FMA
+// scales it by 2^127 or 2^123 and subtracts z.
 __device__ __forceinline__ void unpack8(uint32_t w, uint32_t zc, uint32_t (&p)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) p[j] = sub_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, zc);
+  const uint32_t v = w >> 8;
+  p[0] = fma_bf16x2(w & 0x000F000Fu, 0x7F007F00u, zc);
+  p[1] = fma_bf16x2(w & 0x00F000F0u, 0x7D007D00u, zc);
+  p[2] = fma_bf16x2(v & 0x000F000Fu, 0x7F007F00u, zc);
+  p[3] = fma_bf16x2(v & 0x00F000F0u, 0x7D007D00u, zc);
+}
+
+// The BF16 pair -z / 64.
+__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
+  const float f = -0.015625f * (float)z;
+  const uint32_t h = __float_as_uint(f) & 0xFFFF0000u;
+  return h | (h >> 16);
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -84,6 +102,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same from a zero accumulator
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 template <int W>
@@ -101,17 +126,19 @@ struct Item {
   int row0, cnt;  // first grouped row, rows (at most 8 NT)
 };
 
+// G: group.  RT: most 16-row tiles of an item.  NT: 8-row activation tiles.
 template <int G, int RT, int NT>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     w4g_gemv_kernel(const __grid_constant__ CUtensorMap tm_q, const W4gArgs g, const GemvCfg c,
                     int* __restrict__ status) {
-  constexpr int W = G / 32;           // words per lane, row and group
-  constexpr int GC = kChunk / G;      // groups per chunk
-  constexpr int SPL = (GC + 3) / 4;   // scales per lane, row and chunk
+  constexpr int W = G / 32;                     // words per lane, row and group
+  constexpr int GS = kChunk / G / NT;           // groups per segment
+  constexpr int SEG = kChunk / NT;              // elements of K per segment
+  constexpr int LG = GS >= 2 ? GS / 2 : 1;      // groups whose scales one lane loads
   constexpr int TOK = 8 * NT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const GemvSmem L = gemv_smem(RT, NT, c.slots, g.experts);
+  const GemvSmem L = gemv_smem(RT, NT, G, c.slots, g.experts);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = warp / c.ks, wk = warp - grp * c.ks;
   const int ngrp = kWarps / c.ks;
@@ -119,14 +146,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   int* s_off = reinterpret_cast<int*>(smem + L.off);
   int* s_pre = reinterpret_cast<int*>(smem + L.pre);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L.abort_flag);
-  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (uint32_t)c.slots * L.slot_bytes;
+  uint8_t* ring = smem + (size_t)warp * (size_t)c.slots * kSlotBytes;
+  const uint32_t ring_s = smem_u32(ring);
+  const uint32_t meta_s = smem_u32(smem) + L.meta + (uint32_t)warp * (uint32_t)GS * 128u;
 
-  if (threadIdx.x == 0) *abort_flag = 0;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    tma_prefetch_desc(&tm_q);
+  }
   if (lane == 0) {
     for (int s = 0; s < c.slots; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) tma_prefetch_desc(&tm_q);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -165,6 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   const int items = s_pre[g.experts];
   const int step = (int)gridDim.x * ngrp;
   const int first = (int)blockIdx.x * ngrp + grp;
+  const int rb = c.tr * c.rt;  // weight rows of an item
 
   auto find = [&](int i) {
     Item t;
@@ -178,59 +210,154 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
     t.e = lo;
     const int rows = s_off[lo + 1] - s_off[lo];
-    const int tiles = (rows + TOK - 1) / TOK;
     const int local = i - s_pre[lo];
-    t.blk = local / tiles;
-    const int tile = local - t.blk * tiles;
+    int tile = 0;
+    t.blk = local;
+    if (rows > TOK) {  // the tiles of one block are neighbours
+      const int tiles = (rows + TOK - 1) / TOK;
+      t.blk = local / tiles;
+      tile = local - t.blk * tiles;
+    }
     t.row0 = s_off[lo] + tile * TOK;
     t.cnt = min(TOK, rows - tile * TOK);
     return t;
   };
 
-  // the warp's issue position: next (item, chunk) to request
-  int iss_item = first, iss_c = wk, iss_y = 0;
-  uint32_t issued = 0, used = 0;
+  // the warp's issue position: the next (item, chunk, tile) to request
+  int iss_item = first, iss_c = wk, iss_i = 0, iss_y = 0, iss_s = 0;
+  uint32_t issued = 0;
   if (iss_item < items) {
     const Item t = find(iss_item);
-    iss_y = t.e * g.n + t.blk * c.rb;
+    iss_y = t.e * g.n + t.blk * rb;
   }
   auto issue = [&]() {
     if (iss_item >= items) return;
-    const uint32_t s = issued % (uint32_t)c.slots;
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bars[s], (uint32_t)c.rb * kChunkBytes);
-      tma_load_2d(smem + (ring - smem_u32(smem)) + s * L.slot_bytes, &tm_q, &bars[s], iss_c * kChunkBytes, iss_y);
+      mbar_arrive_expect_tx(&bars[iss_s], (uint32_t)c.tr * kChunkBytes);
+      tma_load_2d(ring + (size_t)iss_s * kSlotBytes, &tm_q, &bars[iss_s], iss_c * kChunkBytes, iss_y + iss_i * c.tr);
     }
     ++issued;
+    if (++iss_s == c.slots) iss_s = 0;
+    if (++iss_i < c.rt) return;
+    iss_i = 0;
     iss_c += c.ks;
-    if (iss_c >= c.chunks) {
-      iss_c = wk;
-      iss_item += step;
-      if (iss_item < items) {
-        const Item t = find(iss_item);
-        iss_y = t.e * g.n + t.blk * c.rb;
-      }
+    if (iss_c < c.chunks) return;
+    iss_c = wk;
+    iss_item += step;
+    if (iss_item < items) {
+      const Item t = find(iss_item);
+      iss_y = t.e * g.n + t.blk * rb;
     }
   };
-  if (wk < c.chunks)
-    for (int s = 0; s < c.slots; ++s) issue();
+  for (int s = 0; s < c.slots; ++s) issue();
 
   const int t4 = lane & 3, g8 = lane >> 2;
   const int r8 = ((g8 & 1) << 2) | (g8 & 2) | (g8 >> 2);  // bit reversal
   const int groups = g.k / G;
-  bool dead = false;
-  for (int it = first; it < items; it += step) {
-    const Item t = find(it);
-    const int n0 = t.blk * c.rb;
-    const uint16_t* ap[NT];
+
+  // The activation rows of an item: row tt * 8 + g8 in this lane.
+  struct Rows {
+    const uint16_t* p[NT];
+  };
+  auto rows_of = [&](const Item& t) {
+    Rows x;
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) {
       const int r = tt * 8 + g8;
-      ap[tt] = nullptr;
+      x.p[tt] = nullptr;
       if (r < t.cnt) {
         const long long src = g.rows ? (long long)g.rows[t.row0 + r] : (long long)t.row0 + r;
-        if (src >= 0 && src < g.a_rows) ap[tt] = g.a + (size_t)src * (size_t)g.k;
+        if (src >= 0 && src < g.a_rows) x.p[tt] = g.a + (size_t)src * (size_t)g.k + t4 * (G / 4);
       }
+    }
+    return x;
+  };
+  // One segment's activations: of each group, this lane's G/4 elements.
+  struct Acts {
+    uint4 v[NT][GS][W];
+  };
+  auto load_acts = [&](const Rows& r, int gi0) {
+    Acts x;
+#pragma unroll
+    for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+      for (int gi = 0; gi < GS; ++gi)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          x.v[tt][gi][w] = make_uint4(0, 0, 0, 0);
+          if (r.p[tt] && gi0 + gi < groups)
+            x.v[tt][gi][w] = __ldg(reinterpret_cast<const uint4*>(r.p[tt] + (size_t)(gi0 + gi) * G + w * 8));
+        }
+    return x;
+  };
+  // Scales and zero points of one tile and segment: lane l has row l % 16,
+  // groups (l / 16) LG ...
+  const int mrow = lane & 15, mhalf = lane >> 4;
+  struct alignas(8) Meta {
+    alignas(8) uint16_t s[LG];
+    alignas(4) uint8_t z[LG];
+  };
+  auto load_meta = [&](const Item& t, int gi0, int i) {
+    Meta m;
+    const int n = t.blk * rb + i * c.tr + mrow;
+    const int gi = gi0 + mhalf * LG;
+    const size_t at = ((size_t)t.e * g.n + n) * (size_t)groups + gi;
+    const bool row_ok = mrow < c.tr && n < g.n && mhalf * LG < GS;
+#pragma unroll
+    for (int v = 0; v < LG; ++v) {
+      m.s[v] = 0;
+      m.z[v] = 8;
+    }
+    if (LG > 1 && c.vec) {
+      if (row_ok && gi < groups) {
+        if constexpr (LG == 2) {
+          *reinterpret_cast<uint32_t*>(m.s) = *reinterpret_cast<const uint32_t*>(g.scale + at);
+          if (g.zero) *reinterpret_cast<uint16_t*>(m.z) = *reinterpret_cast<const uint16_t*>(g.zero + at);
+        } else if constexpr (LG == 4) {
+          *reinterpret_cast<uint2*>(m.s) = *reinterpret_cast<const uint2*>(g.scale + at);
+          if (g.zero) *reinterpret_cast<uint32_t*>(m.z) = *reinterpret_cast<const uint32_t*>(g.zero + at);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < LG; ++v)
+        if (row_ok && gi + v < groups) {
+          m.s[v] = g.scale[at + v];
+          if (g.zero) m.z[v] = g.zero[at + v];
+        }
+    }
+    return m;
+  };
+  // ... to shared memory, per group and mma row pair: {s(r), s(r + 8), -z/64
+  // of r, of r + 8}
+  auto put_meta = [&](const Meta& m) {
+    if (mhalf * LG >= GS) return;
+    const uint32_t at = meta_s + (uint32_t)(mhalf * LG) * 128u + (uint32_t)(mrow & 7) * 16u + (uint32_t)(mrow >> 3) * 4u;
+#pragma unroll
+    for (int v = 0; v < LG; ++v) {
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 128u * v), "f"(scale_f32(m.s[v], g.half_scale)) : "memory");
+      if (g.zero) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 128u * v + 8u), "r"(zero_pair(m.z[v])) : "memory");
+    }
+  };
+
+  bool dead = false;
+  Item next = {};
+  Rows next_rows = {};
+  Meta meta = {};
+  if (first < items) {
+    next = find(first);
+    next_rows = rows_of(next);
+    meta = load_meta(next, wk * GS * NT, 0);
+  }
+  int slot = 0;
+  uint32_t phase = 0;
+  for (int it = first; it < items; it += step) {
+    const Item t = next;
+    const Rows rows = next_rows;
+    const int n0 = t.blk * rb;
+    if (it + step < items) {
+      next = find(it + step);
+      next_rows = rows_of(next);
     }
     float tot[RT][NT][4];
 #pragma unroll
@@ -241,130 +368,120 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         for (int j = 0; j < 4; ++j) tot[i][tt][j] = 0.0f;
 
     for (int ch = wk; ch < c.chunks; ch += c.ks) {
-      const int gbase = ch * GC;
-      // scales and zero points: lane t4 holds groups t4 (and t4 + 4) of its rows
-      uint16_t sc[RT][2][SPL];
-      uint8_t zp[RT][2][SPL];
+      const bool last = ch + c.ks >= c.chunks;
+      const int slot0 = slot;  // the chunk's first tile
+      const uint32_t phase0 = phase;
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int v = 0; v < SPL; ++v) {
-            const int gi = gbase + v * 4 + t4;
-            const int n = n0 + i * 16 + h * 8 + r8;
-            sc[i][h][v] = 0;
-            zp[i][h][v] = 8;
-            if (v * 4 + t4 < GC && gi < groups && n < g.n) {
-              const size_t at = ((size_t)t.e * g.n + n) * (size_t)groups + gi;
-              sc[i][h][v] = g.scale[at];
-              if (g.zero) zp[i][h][v] = g.zero[at];
-            }
-          }
-      // activations of the chunk: lane t4 of each group's G/4 elements
-      uint4 x[NT][GC][W];
-#pragma unroll
-      for (int tt = 0; tt < NT; ++tt)
-#pragma unroll
-        for (int gi = 0; gi < GC; ++gi)
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            x[tt][gi][w] = make_uint4(0, 0, 0, 0);
-            if (ap[tt] && gbase + gi < groups)
-              x[tt][gi][w] =
-                  __ldg(reinterpret_cast<const uint4*>(ap[tt] + (size_t)(gbase + gi) * G + t4 * (G / 4) + w * 8));
-          }
-      const uint32_t s = used % (uint32_t)c.slots;
-      bool landed = !dead;
-      if (!dead)
-        landed = mbar_wait(&bars[s], (used / (uint32_t)c.slots) & 1u, abort_flag, status, DEV_ERR_TIMEOUT_DECODE);
-      if (__any_sync(0xFFFFFFFFu, !landed)) dead = true;
-      const uint32_t slot = ring + s * L.slot_bytes;
-#pragma unroll
-      for (int gi = 0; gi < GC; ++gi) {
-        if (gbase + gi >= groups) break;
-        uint32_t b[NT][W][4];
+      for (int seg = 0; seg < NT; ++seg) {
+        const int gbase = (ch * NT + seg) * GS;
+        // where the next segment's scales are
+        const bool same = seg + 1 < NT || !last;
+        const int gnext = seg + 1 < NT ? gbase + GS : (last ? wk : ch + c.ks) * NT * GS;
+        const Acts acts = load_acts(rows, gbase);
+        uint32_t b[NT][GS][W][4];
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const uint4 v = x[tt][gi][w];
-            b[tt][w][0] = __byte_perm(v.x, v.z, 0x5410);
-            b[tt][w][1] = __byte_perm(v.x, v.z, 0x7632);
-            b[tt][w][2] = __byte_perm(v.y, v.w, 0x5410);
-            b[tt][w][3] = __byte_perm(v.y, v.w, 0x7632);
-          }
-        const int src = (lane & ~3) | (gi & 3);
-        const uint32_t boff = (uint32_t)(gi * (G / 2) + t4 * (G / 8));
+          for (int gi = 0; gi < GS; ++gi)
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+              const uint4 v = acts.v[tt][gi][w];
+              b[tt][gi][w][0] = __byte_perm(v.x, v.z, 0x5410);
+              b[tt][gi][w][1] = __byte_perm(v.x, v.z, 0x7632);
+              b[tt][gi][w][2] = __byte_perm(v.y, v.w, 0x5410);
+              b[tt][gi][w][3] = __byte_perm(v.y, v.w, 0x7632);
+            }
+        slot = slot0;
+        phase = phase0;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-          uint32_t zc[2];
-          float sv[2];
-          uint32_t w0[W], w1[W];
-          const uint32_t ra = (uint32_t)(i * 16 + r8);
-          const uint32_t at = slot + ra * kChunkBytes + ((((boff >> 4) ^ (uint32_t)r8) << 4) | (boff & 15u));
-          lds_words<W>(at, w0);
-          lds_words<W>(at + 8u * kChunkBytes, w1);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            sv[h] = scale_f32((uint16_t)__shfl_sync(0xFFFFFFFFu, (int)sc[i][h][gi / 4], src), g.half_scale);
-            zc[h] = (g.zero ? (uint32_t)__shfl_sync(0xFFFFFFFFu, (int)zp[i][h][gi / 4], src) : 8u) * 0x00010001u |
-                    0x43004300u;
-          }
-          float d[NT][4];
-#pragma unroll
-          for (int tt = 0; tt < NT; ++tt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[tt][j] = 0.0f;
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            uint32_t p0[4], p1[4];
-            unpack8(w0[w], zc[0], p0);
-            unpack8(w1[w], zc[1], p1);
-#pragma unroll
-            for (int tt = 0; tt < NT; ++tt) {
-              mma_bf16(d[tt], p0[0], p1[0], p0[1], p1[1], b[tt][w][0], b[tt][w][1]);
-              mma_bf16(d[tt], p0[2], p1[2], p0[3], p1[3], b[tt][w][2], b[tt][w][3]);
+          if (i < c.rt) {
+            __syncwarp();
+            put_meta(meta);
+            __syncwarp();
+            const bool tile_last = i + 1 == c.rt;
+            meta = load_meta(tile_last && !same ? next : t, tile_last ? gnext : gbase, tile_last ? 0 : i + 1);
+            if (seg == 0 && !dead) {
+              const bool landed = mbar_wait(&bars[slot], phase, abort_flag, status, DEV_ERR_TIMEOUT_DECODE);
+              if (__any_sync(0xFFFFFFFFu, !landed)) dead = true;
             }
-          }
+            const uint32_t sl = ring_s + (uint32_t)slot * kSlotBytes + (uint32_t)r8 * kChunkBytes;
 #pragma unroll
-          for (int tt = 0; tt < NT; ++tt) {
-            tot[i][tt][0] = fmaf(d[tt][0], sv[0], tot[i][tt][0]);
-            tot[i][tt][1] = fmaf(d[tt][1], sv[0], tot[i][tt][1]);
-            tot[i][tt][2] = fmaf(d[tt][2], sv[1], tot[i][tt][2]);
-            tot[i][tt][3] = fmaf(d[tt][3], sv[1], tot[i][tt][3]);
+            for (int gi = 0; gi < GS; ++gi) {
+              uint32_t w0[W], w1[W];
+              const uint32_t boff = (uint32_t)(seg * (SEG / 2) + gi * (G / 2) + t4 * (G / 8));
+              const uint32_t at = sl + ((((boff >> 4) ^ (uint32_t)r8) << 4) | (boff & 15u));
+              lds_words<W>(at, w0);
+              lds_words<W>(at + 8u * kChunkBytes, w1);
+              float s0, s1;
+              uint32_t z0 = 0xBE00BE00u, z1 = 0xBE00BE00u;  // -8 / 64
+              const uint32_t ma = meta_s + (uint32_t)gi * 128u + (uint32_t)r8 * 16u;
+              asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(s0), "=f"(s1) : "r"(ma));
+              if (g.zero) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(z0), "=r"(z1) : "r"(ma + 8u));
+              float d[NT][4];
+#pragma unroll
+              for (int w = 0; w < W; ++w) {
+                uint32_t p0[4], p1[4];
+                unpack8(w0[w], z0, p0);
+                unpack8(w1[w], z1, p1);
+#pragma unroll
+                for (int tt = 0; tt < NT; ++tt) {
+                  if (w == 0)
+                    mma_bf16_first(d[tt], p0[0], p1[0], p0[1], p1[1], b[tt][gi][w][0], b[tt][gi][w][1]);
+                  else
+                    mma_bf16(d[tt], p0[0], p1[0], p0[1], p1[1], b[tt][gi][w][0], b[tt][gi][w][1]);
+                  mma_bf16(d[tt], p0[2], p1[2], p0[3], p1[3], b[tt][gi][w][2], b[tt][gi][w][3]);
+                }
+              }
+#pragma unroll
+              for (int tt = 0; tt < NT; ++tt) {
+                tot[i][tt][0] = fmaf(d[tt][0], s0, tot[i][tt][0]);
+                tot[i][tt][1] = fmaf(d[tt][1], s0, tot[i][tt][1]);
+                tot[i][tt][2] = fmaf(d[tt][2], s1, tot[i][tt][2]);
+                tot[i][tt][3] = fmaf(d[tt][3], s1, tot[i][tt][3]);
+              }
+            }
+            if (++slot == c.slots) {
+              slot = 0;
+              phase ^= 1u;
+            }
+            if (seg + 1 == NT) {
+              // every lane has read the slot: it may be refilled (async proxy)
+              __syncwarp();
+              if (!dead) {
+                fence_proxy_async_smem();
+                issue();
+              }
+            }
           }
         }
       }
-      ++used;
-      // every lane has read the slot: it may be refilled (async proxy)
-      __syncwarp();
-      if (!dead) {
-        fence_proxy_async_smem();
-        issue();
-      }
     }
 
-    // sum of the item's ks warps, in warp order
-    constexpr int PITCH = RT * 16 + 1;
+    // sum of the item's ks warps, in warp order; the codes were taken / 64
+    constexpr int PITCH = RT * 16;
     float* red = reinterpret_cast<float*>(smem + L.red);
     float* mine = red + (size_t)warp * PITCH * TOK;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
+      if (i < c.rt) {
 #pragma unroll
-      for (int tt = 0; tt < NT; ++tt)
+        for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mine[(tt * 8 + t4 * 2 + (j & 1)) * PITCH + i * 16 + (j >> 1) * 8 + r8] = tot[i][tt][j];
+          for (int j = 0; j < 4; ++j)
+            mine[(tt * 8 + t4 * 2 + (j & 1)) * PITCH + i * 16 + (j >> 1) * 8 + r8] = tot[i][tt][j];
+      }
     const int bar_threads = c.ks * 32;
     asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(bar_threads) : "memory");
-    const int nrows = min(c.rb, g.n - n0);
     const float* part = red + (size_t)grp * c.ks * PITCH * TOK;
-    for (int i = wk * 32 + lane; i < nrows * t.cnt; i += bar_threads) {
-      const int tok = i / nrows, r = i - tok * nrows;
+    for (int i = wk * 32 + lane; i < PITCH * t.cnt; i += bar_threads) {
+      const int tok = i / PITCH, r = i & (PITCH - 1);
+      const int row = n0 + (r >> 4) * c.tr + (r & 15);
+      if ((r >> 4) >= c.rt || (r & 15) >= c.tr || row >= g.n) continue;
       float v = 0.0f;
       for (int w = 0; w < c.ks; ++w) v += part[((size_t)w * TOK + tok) * PITCH + r];
-      reinterpret_cast<__nv_bfloat16*>(g.out)[(size_t)(t.row0 + tok) * (size_t)g.n + n0 + r] = __float2bfloat16_rn(v);
+      reinterpret_cast<__nv_bfloat16*>(g.out)[(size_t)(t.row0 + tok) * (size_t)g.n + row] =
+          __float2bfloat16_rn(64.0f * v);
     }
     asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(bar_threads) : "memory");
   }
@@ -413,12 +530,16 @@ cudaError_t launch(const CUtensorMap& tm, const W4gArgs& g, const GemvCfg& c, in
 template <int G>
 cudaError_t launch_g(const CUtensorMap& tm, const W4gArgs& g, const W4gGemvPlan& p, int* status,
                      cudaStream_t stream) {
-  const GemvCfg c = {p.rb, p.ks, p.slots, p.nblk, p.chunks};
-  if (p.rt == 1)
-    return p.nt == 1 ? launch<G, 1, 1>(tm, g, c, p.grid, p.smem, status, stream)
-                     : launch<G, 1, 2>(tm, g, c, p.grid, p.smem, status, stream);
-  return p.nt == 1 ? launch<G, 2, 1>(tm, g, c, p.grid, p.smem, status, stream)
-                   : launch<G, 2, 2>(tm, g, c, p.grid, p.smem, status, stream);
+  GemvCfg c = {p.tr, p.rt, p.ks, p.slots, p.nblk, p.chunks, 0};
+  // a lane's scales start at a multiple of `lg` groups of its row
+  const int gs = kChunk / G / p.nt, lg = gs >= 2 ? gs / 2 : 1;
+  c.vec = (g.k / G) % lg == 0 && reinterpret_cast<uintptr_t>(g.scale) % (2u * lg) == 0 &&
+          reinterpret_cast<uintptr_t>(g.zero) % (unsigned)lg == 0;
+  if (p.rt <= 2)
+    return p.nt == 1 ? launch<G, 2, 1>(tm, g, c, p.grid, p.smem, status, stream)
+                     : launch<G, 2, 2>(tm, g, c, p.grid, p.smem, status, stream);
+  return p.nt == 1 ? launch<G, 4, 1>(tm, g, c, p.grid, p.smem, status, stream)
+                   : launch<G, 4, 2>(tm, g, c, p.grid, p.smem, status, stream);
 }
 
 }  // namespace
@@ -434,24 +555,30 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   p.nt = (g.rows_max + active - 1) / active <= 8 ? 1 : 2;
   const long long tok = 8 * p.nt;
   const long long tiles = active + (g.rows_max - active) / tok;
-  // rows per item: the fewest row steps over whole waves of two CTAs per SM
+  // rt tiles of tr rows per item: the least estimated time over whole waves
+  // of two CTAs per SM
   const long long slots_all = 2LL * num_sms * ngrp;
   double best = 0.0;
-  for (int rb = 32; rb >= 8; rb -= 2) {
-    const long long items = ((g.n + rb - 1) / rb) * tiles;
-    const long long waves = (items + slots_all - 1) / slots_all;
-    const double cost = (double)waves * (rb + 4);
-    if (best == 0.0 || cost < best - 1e-9) {
-      best = cost;
-      p.rb = rb;
+  for (int rt = 4; rt >= 1; --rt)
+    for (int tr = 16; tr >= 8; --tr) {
+      const int rb = rt * tr;
+      const long long items = ((g.n + rb - 1) / rb) * tiles;
+      const long long waves = (items + slots_all - 1) / slots_all;
+      const double cost = (double)waves * ((rb > 13 * rt ? rb : 13 * rt) + 8);
+      if (best == 0.0 || cost < best - 1e-9) {
+        best = cost;
+        p.rt = rt;
+        p.tr = tr;
+      }
     }
-  }
-  p.rt = p.rb <= 16 ? 1 : 2;
-  p.nblk = (g.n + p.rb - 1) / p.rb;
-  // slots: as many as leave room for two CTAs per SM (228 KB less 1 KB per CTA)
+  const int rb = p.rt * p.tr;
+  p.nblk = (g.n + rb - 1) / rb;
+  // slots: as many as leave room for two CTAs per SM (228 KB less 1 KB per
+  // CTA), at least one more than a chunk's tiles
+  const int rt_max = p.rt <= 2 ? 2 : 4;
   p.slots = 6;
-  while (p.slots > 2 && gemv_smem(p.rt, p.nt, p.slots, g.experts).total > 115712u) --p.slots;
-  p.smem = gemv_smem(p.rt, p.nt, p.slots, g.experts).total;
+  while (p.slots > p.rt + 1 && gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total > 115712u) --p.slots;
+  p.smem = gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total;
   const long long items = (long long)p.nblk * (tiles + active);  // ragged tails add at most one tile per expert
   const long long ctas = (items + ngrp - 1) / ngrp;
   p.grid = (int)(ctas < 2LL * num_sms ? ctas : 2LL * num_sms);
