@@ -37,7 +37,16 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms);
 cudaError_t launch_w4g_gemv(const CUtensorMap& tm_q, const W4gArgs& g, const W4gGemvPlan& p, int* status,
                             cudaStream_t stream);
 
-cudaError_t launch_w4g_simple(const W4gArgs& g, cudaStream_t stream);
+// Many rows per expert: the tcgen05 tensor cores, tiles of 128 weight rows x
+// bm activation rows.  Tensor maps: codes [experts * N, K/2] bytes, box 128
+// rows x 32 bytes, 32-byte swizzle; activations [a_rows, K] BF16, box bm rows
+// (one row with an index) x 64, 128-byte swizzle.
+struct W4gGemmPlan {
+  int bm, grid;
+};
+W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms);
+cudaError_t launch_w4g_gemm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,
+                            int* status, cudaStream_t stream);
 
 // Router.  Blocks of route_block_tokens(tokens) tokens; scratch holds one
 // row of `experts` counts per block (none when there is one block).

@@ -1,0 +1,627 @@
+// Integer 4-bit projections on the 5th-generation tensor cores, rows grouped
+// by expert with ragged sizes (dense: one expert):
+//   out[r, n] = bf16( sum_g s[n, g] * P[r, n, g] ),
+//   P = sum_{k in g} a[r, k] * (q[n, k] - z[n, g])
+// BF16 activations x BF16 integers (exact), float32 accumulation in tensor
+// memory per group, one float32 FMA per element and group outside it.
+//
+// Tile: 128 weight rows (tensor-memory lanes, MMA M) x BM activation rows of
+// one expert (columns, MMA N).  The codes are the A operand and go through
+// tensor memory: a stage's codes (128 rows x 64 elements, 4 KB) come by TMA,
+// eight warps unpack them to BF16 pairs (12 instructions per 8 elements) and
+// store them with tcgen05.st as the A operand of `tcgen05.mma kind::f16`.
+// Through shared memory the unpacked tile (16 KB per stage, written once and
+// read once) would compete with the activation tile for its bandwidth.
+// Activations (B operand) come by TMA into 128-byte-swizzled tiles, the rows
+// of a gathered tile four at a time (tile::gather4).
+//
+// The scale changes every G elements of K, so each group accumulates into its
+// own tensor-memory buffer (a ring of 384 / BM) and the epilogue adds s * P
+// to float32 registers: a thread owns one weight row, so the scale is one
+// register, and BM / 2 columns.  Per SM and group that is 128 x BM FMAs (two
+// per instruction) against BM x G x 128 tensor FMAs: hidden for G = 64 and
+// 128; at G = 32 the unpacking and the rescale together fill the issue slots.
+//
+// Tiles are dealt to persistent CTAs in order of expert, weight tile,
+// activation tile (activation fastest, so that CTAs running together read the
+// same weight tile), from offsets read on the device.
+//
+// Warps (20): 0 loads, 1 MMAs (one thread; owns the tensor memory), 2-3 idle,
+// 4-11 unpack (warp w: lanes 32 (w % 4).., K half (w - 4) / 4 of a stage),
+// 12-19 epilogue (lanes 32 (w % 4).., column half).  Every wait is bounded: a
+// wait that runs out sets a status bit and every role leaves its loop; copies
+// and MMAs in flight are drained (bounded) before the tensor memory is freed.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "w4g.h"
+
+namespace bsr {
+namespace {
+
+constexpr int kBn = 128;       // weight rows per tile
+constexpr int kKs = 64;        // elements of K per stage
+constexpr int kRaw = kBn * kKs / 2;
+constexpr int kThreads = 640;
+constexpr int kDeqWarp0 = 4, kEpiWarp0 = 12;
+constexpr int kDeqWarps = 8, kEpiWarps = 8;
+constexpr int kAStages = 4;    // unpacked stages in tensor memory, 32 columns each
+constexpr uint32_t kColA = 384, kTmemCols = 512;
+constexpr int kMaxStages = 12;
+constexpr size_t kSmemMax = 232448;
+// register split: launched with 96 per thread
+constexpr int kLaunchRegs = 96, kCtrlRegs = 40, kDeqRegs = 48, kEpiRegs = 168;
+static_assert(128 * kCtrlRegs + 256 * kDeqRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
+
+template <int BM>
+struct Cfg {
+  static constexpr int TBUF = 384 / BM < 6 ? 384 / BM : 6;
+  static constexpr int COLS = BM / 2;                 // columns per epilogue warp
+  static constexpr int STAGE = kRaw + BM * 128;
+};
+
+struct Ctrl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t aready[kAStages], afree[kAStages];
+  uint64_t tfull[6], tempty[6];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// kind::f16, D = F32, A = B = BF16, both K-major.
+constexpr uint32_t idesc_bf16(int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] x B[smem]^T
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Four rows of a 2-D tensor, 512 bytes of the tile.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int32_t x, int4 y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+      "%5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Ties registers written by a tensor-memory load to this point of the
+// program (after tcgen05.wait::ld).
+__device__ __forceinline__ void regs_after_wait(uint32_t (&r)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                      "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// The BF16 pair -z / 64.
+__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
+  const uint32_t h = __float_as_uint(-0.015625f * (float)z) & 0xFFFF0000u;
+  return h | (h >> 16);
+}
+
+__device__ __forceinline__ float scale_f32(uint16_t s, int half) {
+  return half ? __half2float(__ushort_as_half(s)) : __uint_as_float((uint32_t)s << 16);
+}
+
+// Bounded wait that ignores the abort flag (used while draining).
+__device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  return true;
+}
+
+struct TileAt {
+  int e, n0, row0, cnt;
+};
+
+// Ring position.
+struct Pos {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+template <int BM, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    w4g_gemm_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_a,
+                    const W4gArgs g, const int stages, int* __restrict__ status) {
+  using C = Cfg<BM>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + (size_t)stages * C::STAGE);
+  int* s_off = reinterpret_cast<int*>(ctrl + 1);
+  int* s_pre = s_off + g.experts + 1;
+  volatile int* abort_flag = &ctrl->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_tiles = (g.n + kBn - 1) / kBn;
+  const int kstages = (g.k + kKs - 1) / kKs;
+  const int groups = g.k / G;
+  // a stage: the activation tile, then the codes
+  auto stage_ptr = [&](int s) { return smem + (size_t)s * C::STAGE; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1 + kDeqWarps);  // the MMA commit + the unpacking warps
+    }
+    for (int s = 0; s < kAStages; ++s) {
+      mbar_init(&ctrl->aready[s], kDeqWarps);
+      mbar_init(&ctrl->afree[s], 1);
+    }
+    for (int b = 0; b < C::TBUF; ++b) {
+      mbar_init(&ctrl->tfull[b], 1);
+      mbar_init(&ctrl->tempty[b], kEpiWarps);
+    }
+    mbar_init(&ctrl->drain, 1);
+    ctrl->abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_a);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctrl->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // tiles before each expert; the offsets clamped to [the one before, R]
+  if (warp == 0) {
+    int edge = 0, sum = 0;
+    const int rows_max = (int)g.rows_max;
+    for (int e0 = 0; e0 < g.experts; e0 += 32) {
+      const int e = e0 + lane;
+      int hi = 0;
+      if (e < g.experts) hi = g.offsets ? g.offsets[e + 1] : rows_max;
+      hi = min(max(hi, edge), rows_max);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, hi, o);
+        if (lane >= o) hi = max(hi, v);
+      }
+      int lo = __shfl_up_sync(0xFFFFFFFFu, hi, 1);
+      if (lane == 0) lo = edge;
+      int s = e < g.experts ? (int)(((unsigned)(hi - lo) + BM - 1) / BM) * n_tiles : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += v;
+      }
+      if (e < g.experts) {
+        s_off[e + 1] = hi;
+        s_pre[e + 1] = sum + s;
+      }
+      edge = __shfl_sync(0xFFFFFFFFu, hi, 31);
+      sum += __shfl_sync(0xFFFFFFFFu, s, 31);
+    }
+    if (lane == 0) s_off[0] = s_pre[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem_base;
+  const int tiles = s_pre[g.experts];
+  auto find = [&](int i) {
+    TileAt t;
+    int lo = 0, hi = g.experts;  // s_pre[lo] <= i < s_pre[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_pre[mid] <= i)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    t.e = lo;
+    const int rows = s_off[lo + 1] - s_off[lo];
+    const int m_tiles = (int)(((unsigned)rows + BM - 1) / BM);
+    const int local = i - s_pre[lo];
+    const int tn = local / m_tiles;
+    const int first = (local - tn * m_tiles) * BM;
+    t.n0 = tn * kBn;
+    t.row0 = s_off[lo] + first;
+    t.cnt = min(BM, rows - first);
+    return t;
+  };
+
+  if (warp < kDeqWarp0) {
+    setmaxnreg_dec<kCtrlRegs>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- loads
+      Pos p;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        const TileAt t = find(tile);
+        constexpr int QL = (BM / 4 + 31) / 32;  // row quads per lane
+        int4 quad[QL];
+        if (g.rows) {
+#pragma unroll
+          for (int i = 0; i < QL; ++i) {
+            int v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = (i * 32 + lane) * 4 + j;
+              v[j] = (int)g.a_rows;  // out of range: zeros
+              if (r < t.cnt) {
+                const int src = g.rows[t.row0 + r];
+                if (src >= 0 && src < g.a_rows) v[j] = src;
+              }
+            }
+            quad[i] = make_int4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        for (int ks = 0; ks < kstages; ++ks) {
+          if (!mbar_wait(&ctrl->empty[p.i], p.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_TMA)) ok = false;
+          if (__any_sync(0xFFFFFFFFu, !ok)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = stage_ptr(p.i);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&ctrl->full[p.i], C::STAGE);
+            tma_load_2d(st + BM * 128, &tm_q, &ctrl->full[p.i], ks * (kKs / 2), t.e * g.n + t.n0);
+            if (!g.rows) tma_load_2d(st, &tm_a, &ctrl->full[p.i], ks * kKs, t.row0);
+          }
+          __syncwarp();
+          if (g.rows) {
+#pragma unroll
+            for (int i = 0; i < QL; ++i)
+              if (i * 32 + lane < BM / 4)
+                tma_gather4(st + (size_t)(i * 32 + lane) * 512, &tm_a, &ctrl->full[p.i], ks * kKs, quad[i]);
+          }
+          ++it;
+          p.next(stages);
+        }
+      }
+      // copies of the last stages must have landed before the CTA may exit
+      if (lane == 0) {
+        const uint32_t n = (uint32_t)stages;
+        for (uint32_t j = it > n ? it - n : 0u; j < it; ++j)
+          if (!wait_drain(&ctrl->full[j % n], (j / n) & 1u)) break;
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA
+      if (lane == 0) {
+        Pos p, ap, tp;
+        constexpr uint32_t idesc = idesc_bf16(kBn, BM);
+        constexpr int STEPS = G / 16;  // MMAs per group
+        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+          int step = 0;
+          for (int ks = 0; ks < kstages; ++ks) {
+            if (!mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA)) goto mma_done;
+            if (!mbar_wait(&ctrl->aready[ap.i], ap.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA)) goto mma_done;
+            tc_fence_after();
+            const uint32_t b_base = smem_u32(stage_ptr(p.i));
+            const uint32_t a_base = tmem + kColA + (uint32_t)ap.i * 32u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (ks * kKs + j * 16 >= g.k) break;
+              if (step == 0) {
+                if (!mbar_wait(&ctrl->tempty[tp.i], tp.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_MMA))
+                  goto mma_done;
+                tc_fence_after();
+              }
+              mma_ts(tmem + (uint32_t)(tp.i * BM), a_base + (uint32_t)j * 8u, smem_desc_k_sw128(b_base + j * 32), idesc,
+                     step > 0);
+              if (++step == STEPS) {
+                tc_commit(&ctrl->tfull[tp.i]);
+                tp.next(C::TBUF);
+                step = 0;
+              }
+            }
+            tc_commit(&ctrl->empty[p.i]);
+            tc_commit(&ctrl->afree[ap.i]);
+            p.next(stages);
+            ap.next(kAStages);
+          }
+        }
+      mma_done:
+        // every MMA issued so far has completed once this commit arrives
+        tc_commit(&ctrl->drain);
+        wait_drain(&ctrl->drain, 0u);
+      }
+      __syncwarp();
+    }
+  } else if (warp < kEpiWarp0) {
+    setmaxnreg_dec<kDeqRegs>();
+    // ------------------------------------------------------------------ unpack
+    const int q = warp & 3, hk = (warp - kDeqWarp0) >> 2;
+    const int row = q * 32 + lane;
+    // 16-byte half hk of the row's 32 bytes, 32-byte swizzle
+    const uint32_t roff = (uint32_t)(BM * 128 + row * 32 + ((hk ^ ((row >> 2) & 1)) * 16));
+    const uint32_t t_addr = tmem + ((uint32_t)(q * 32) << 16) + kColA + (uint32_t)hk * 16u;
+    Pos p, ap;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      const uint8_t* zrow = nullptr;
+      if (g.zero) {
+        const TileAt t = find(tile);
+        if (t.n0 + row < g.n) zrow = g.zero + ((size_t)t.e * g.n + t.n0 + row) * (size_t)groups;
+      }
+      // zero points of this and the next two stages
+      auto zero_at = [&](int ks) -> uint32_t {
+        const int gi = (ks * kKs + hk * 32) / G;
+        return zrow && gi < groups ? (uint32_t)zrow[gi] : 8u;
+      };
+      uint32_t z0 = 8, z1 = 8, z2 = 8;
+      if (g.zero) {
+        z0 = zero_at(0);
+        z1 = zero_at(1);
+        z2 = zero_at(2);
+      }
+      for (int ks = 0; ks < kstages; ++ks) {
+        uint32_t zc = 0xBE00BE00u;  // -8 / 64
+        if (g.zero) {
+          zc = zero_pair(z0);
+          z0 = z1;
+          z1 = z2;
+          z2 = zero_at(ks + 3);
+        }
+        if (!mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP)) ok = false;
+        if (__any_sync(0xFFFFFFFFu, !ok)) {
+          ok = false;
+          break;
+        }
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(smem_u32(stage_ptr(p.i)) + roff)
+                     : "memory");
+        uint32_t v[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // byte j in both halves: its low nibble in bits 0-3 of the low
+            // half, its high nibble in bits 4-7 of the high half; bits below
+            // 256 read as BF16 are that integer times 2^-133
+            const uint32_t b = __byte_perm(w[i], 0u, j | 0x4040 | (j << 8)) & 0x00F0000Fu;
+            v[i * 4 + j] = fma_bf16x2(b, 0x7D007F00u, zc);
+          }
+        // the codes are in registers: the stage may be refilled as far as
+        // this warp is concerned
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->empty[p.i]);
+        if (!mbar_wait(&ctrl->afree[ap.i], ap.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_PREP)) ok = false;
+        if (__any_sync(0xFFFFFFFFu, !ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st_x16(t_addr + (uint32_t)ap.i * 32u, v);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->aready[ap.i]);
+        p.next(stages);
+        ap.next(kAStages);
+      }
+    }
+  } else {
+    setmaxnreg_inc<kEpiRegs>();
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * C::COLS);
+    constexpr int CH = C::COLS / 16;  // 16-column chunks
+    static_assert(C::COLS % 16 == 0, "whole chunks");
+    float2 acc[CH][8];
+    Pos tp;
+    bool ok = true;
+    // scales of the next four groups of this thread's weight row
+    float sq[4];
+    const uint16_t* srow = nullptr;
+    auto scale_at = [&](int gi) { return srow && gi < groups ? scale_f32(srow[gi], g.half_scale) : 0.0f; };
+    auto open_tile = [&](const TileAt& t) {
+      const int n = t.n0 + q * 32 + lane;
+      srow = n < g.n ? g.scale + ((size_t)t.e * g.n + n) * (size_t)groups : nullptr;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sq[i] = scale_at(i);
+    };
+    TileAt t = {};
+    if ((int)blockIdx.x < tiles) {
+      t = find(blockIdx.x);
+      open_tile(t);
+    }
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[c][j] = make_float2(0.0f, 0.0f);
+      for (int gi = 0; gi < groups; ++gi) {
+        const float2 s2 = make_float2(sq[0], sq[0]);
+        sq[0] = sq[1];
+        sq[1] = sq[2];
+        sq[2] = sq[3];
+        sq[3] = scale_at(gi + 4);
+        if (!mbar_wait(&ctrl->tfull[tp.i], tp.phase, abort_flag, status, DEV_ERR_TIMEOUT_EPI)) ok = false;
+        if (__any_sync(0xFFFFFFFFu, !ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tb = tl + (uint32_t)(tp.i * BM);
+        uint32_t r[2][16];
+        tmem_ld(tb, r[0]);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          tc_wait_ld();
+          regs_after_wait(r[c & 1]);
+          if (c + 1 < CH)
+            tmem_ld(tb + 16u * (c + 1), r[(c + 1) & 1]);
+          else {
+            // the last chunk is in registers: hand the buffer back to the MMA
+            tc_fence_before();
+            mbar_arrive_lane0(&ctrl->tempty[tp.i], lane);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            acc[c][j] = __ffma2_rn(make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1])),
+                                   s2, acc[c][j]);
+        }
+        tp.next(C::TBUF);
+      }
+      if (!ok) break;
+      const TileAt now = t;
+      if (tile + (int)gridDim.x < tiles) {  // the next tile's scales are on their way during the stores
+        t = find(tile + gridDim.x);
+        open_tile(t);
+      }
+      const int n = now.n0 + q * 32 + lane;
+      const int c0 = h * C::COLS;
+      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(g.out) + ((size_t)now.row0 + c0) * (size_t)g.n + n;
+      if (n < g.n) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float v = (j & 1) ? acc[c][j >> 1].y : acc[c][j >> 1].x;
+            if (c0 + c * 16 + j < now.cnt) *o = __float2bfloat16_rn(64.0f * v);  // the codes were taken / 64
+            asm volatile("add.s64 %0, %0, %1;" : "+l"(o) : "l"((long long)g.n * 2));
+          }
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int BM>
+size_t smem_bytes(int stages, int experts) {
+  return 1024 + (size_t)stages * Cfg<BM>::STAGE + sizeof(Ctrl) + 2 * sizeof(int) * ((size_t)experts + 1);
+}
+
+template <int BM>
+int stage_count(int experts) {
+  int s = kMaxStages;
+  while (s > 2 && smem_bytes<BM>(s, experts) > kSmemMax) --s;
+  return s;
+}
+
+std::mutex g_mu;
+
+template <int BM, int G>
+cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, int grid, int* status,
+                   cudaStream_t stream) {
+  auto kern = w4g_gemm_kernel<BM, G>;
+  static bool granted[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!granted[dev]) {
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+      // the register split assumes every thread starts with kLaunchRegs registers
+      if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+      if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax)) != cudaSuccess)
+        return e;
+      granted[dev] = true;
+    }
+  }
+  const int stages = stage_count<BM>(g.experts);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<BM>(stages, g.experts);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_q, tm_a, g, stages, status);
+}
+
+template <int BM>
+cudaError_t launch_bm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, int grid, int* status,
+                      cudaStream_t stream) {
+  switch (g.group) {
+    case 32: return launch<BM, 32>(tm_q, tm_a, g, grid, status, stream);
+    case 64: return launch<BM, 64>(tm_q, tm_a, g, grid, status, stream);
+    case 128: return launch<BM, 128>(tm_q, tm_a, g, grid, status, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms) {
+  W4gGemmPlan p = {};
+  const long long active = g.rows_max < g.experts ? g.rows_max : g.experts;
+  const long long n_tiles = (g.n + kBn - 1) / kBn;
+  const long long rows = (g.rows_max + active - 1) / active;  // of an expert, on average
+  const int widths[4] = {192, 128, 64, 32};
+  double best = 0.0;
+  for (int bm : widths) {
+    const long long tiles = n_tiles * active * ((rows + bm - 1) / bm);
+    const long long waves = (tiles + num_sms - 1) / num_sms;
+    const double cost = (double)waves * (bm < 80 ? 80 : bm);
+    if (best == 0.0 || cost < best - 1e-9) {
+      best = cost;
+      p.bm = bm;
+    }
+  }
+  const long long most = n_tiles * (active + g.rows_max / p.bm);  // of any grouping
+  p.grid = (int)(most < num_sms ? most : num_sms);
+  return p;
+}
+
+cudaError_t launch_w4g_gemm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,
+                            int* status, cudaStream_t stream) {
+  switch (p.bm) {
+    case 32: return launch_bm<32>(tm_q, tm_a, g, p.grid, status, stream);
+    case 64: return launch_bm<64>(tm_q, tm_a, g, p.grid, status, stream);
+    case 128: return launch_bm<128>(tm_q, tm_a, g, p.grid, status, stream);
+    case 192: return launch_bm<192>(tm_q, tm_a, g, p.grid, status, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace bsr
