@@ -153,7 +153,7 @@ bsr_status run_product(const bsr::W4gArgs& g, void* stream) {
   if ((st = encode_2d(&tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, (uint64_t)g.k / 2, (uint64_t)g.experts * g.n,
                       (uint64_t)g.k / 2, 32, 128, CU_TENSOR_MAP_SWIZZLE_32B, "w4g codes")) != BSR_OK ||
       (st = encode_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.a, (uint64_t)g.k, (uint64_t)g.a_rows,
-                      (uint64_t)g.k * 2, 64, g.rows ? 1u : (uint32_t)p.bm, CU_TENSOR_MAP_SWIZZLE_128B,
+                      (uint64_t)g.k * 2, 64, (uint32_t)p.bm, CU_TENSOR_MAP_SWIZZLE_128B,
                       "w4g activations")) != BSR_OK)
     return st;
   return cuda_status(bsr::launch_w4g_gemm(tm_q, tm_a, g, p, d.status, as_stream(stream)), "w4g projection launch");

@@ -8,12 +8,13 @@
 // Tile: 128 weight rows (tensor-memory lanes, MMA M) x BM activation rows of
 // one expert (columns, MMA N).  The codes are the A operand and go through
 // tensor memory: a stage's codes (128 rows x 64 elements, 4 KB) come by TMA,
-// eight warps unpack them to BF16 pairs (12 instructions per 8 elements) and
-// store them with tcgen05.st as the A operand of `tcgen05.mma kind::f16`.
+// two sets of four warps unpack alternate stages to BF16 pairs (12
+// instructions per 8 elements) and store them with tcgen05.st as the A operand of `tcgen05.mma kind::f16`.
 // Through shared memory the unpacked tile (16 KB per stage, written once and
 // read once) would compete with the activation tile for its bandwidth.
-// Activations (B operand) come by TMA into 128-byte-swizzled tiles, the rows
-// of a gathered tile four at a time (tile::gather4).
+// Activations (B operand) come by TMA into 128-byte-swizzled tiles; the rows
+// of a gathered tile by 16-byte asynchronous copies of two warps (TMA's
+// four-row gathers took 73 cycles each to issue, 32 and more per stage).
 //
 // The scale changes every G elements of K, so each group accumulates into its
 // own tensor-memory buffer (a ring of 384 / BM) and the epilogue adds s * P
@@ -26,9 +27,8 @@
 // activation tile (activation fastest, so that CTAs running together read the
 // same weight tile), from offsets read on the device.
 //
-// Warps (20): 0 loads, 1 MMAs (one thread; owns the tensor memory), 2-3 idle,
-// 4-11 unpack (warp w: lanes 32 (w % 4).., K half (w - 4) / 4 of a stage),
-// 12-19 epilogue (lanes 32 (w % 4).., column half).  Every wait is bounded: a
+// Warps (20): 0 TMA loads, 1 MMAs (one elected lane; owns the tensor memory),
+// 2-3 gathered rows, 4-11 unpack (warp w: lanes 32 (w % 4)..), 12-19 epilogue (lanes 32 (w % 4).., column half).  Every wait is bounded: a
 // wait that runs out sets a status bit and every role leaves its loop; copies
 // and MMAs in flight are drained (bounded) before the tensor memory is freed.
 #include <cuda_bf16.h>
@@ -47,13 +47,14 @@ constexpr int kKs = 64;        // elements of K per stage
 constexpr int kRaw = kBn * kKs / 2;
 constexpr int kThreads = 640;
 constexpr int kDeqWarp0 = 4, kEpiWarp0 = 12;
-constexpr int kDeqWarps = 8, kEpiWarps = 8;
+constexpr int kDeqWarps = 8, kEpiWarps = 8, kGatherWarps = 2;
+constexpr int kGatherAhead = 3;  // stages of a gather warp in flight
 constexpr int kAStages = 4;    // unpacked stages in tensor memory, 32 columns each
 constexpr uint32_t kColA = 384, kTmemCols = 512;
 constexpr int kMaxStages = 12;
 constexpr size_t kSmemMax = 232448;
 // register split: launched with 96 per thread
-constexpr int kLaunchRegs = 96, kCtrlRegs = 40, kDeqRegs = 48, kEpiRegs = 168;
+constexpr int kLaunchRegs = 96, kCtrlRegs = 48, kDeqRegs = 48, kEpiRegs = 168;
 static_assert(128 * kCtrlRegs + 256 * kDeqRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
 
 template <int BM>
@@ -65,7 +66,7 @@ struct Cfg {
 
 struct Ctrl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t aready[kAStages], afree[kAStages];
+  uint64_t aready[kAStages];
   uint64_t tfull[6], tempty[6];
   uint64_t drain;
   uint32_t tmem_base;
@@ -83,15 +84,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, 
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Four rows of a 2-D tensor, 512 bytes of the tile.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int32_t x, int4 y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-      "%5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
       : "memory");
 }
 
@@ -145,6 +137,18 @@ __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
+// One lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// 16 bytes global -> shared, zeros if !in.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
 struct TileAt {
   int e, n0, row0, cnt;
 };
@@ -171,8 +175,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + (size_t)stages * C::STAGE);
   int* s_off = reinterpret_cast<int*>(ctrl + 1);
   int* s_pre = s_off + g.experts + 1;
+  int* s_rows = s_pre + g.experts + 1;  // [BM], of the gather warps
   volatile int* abort_flag = &ctrl->abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // through a shuffle, so that the compiler knows it uniform: the roles' loops
+  // then keep their descriptors and addresses in uniform registers
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   const int n_tiles = (g.n + kBn - 1) / kBn;
   const int kstages = (g.k + kKs - 1) / kKs;
   const int groups = g.k / G;
@@ -181,13 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(&ctrl->full[s], 1);
-      mbar_init(&ctrl->empty[s], 1 + kDeqWarps);  // the MMA commit + the unpacking warps
+      mbar_init(&ctrl->full[s], g.rows ? 1 + kGatherWarps : 1);
+      mbar_init(&ctrl->empty[s], 1 + kDeqWarps / 2);  // the MMA commit + the stage's unpacking warps
     }
-    for (int s = 0; s < kAStages; ++s) {
-      mbar_init(&ctrl->aready[s], kDeqWarps);
-      mbar_init(&ctrl->afree[s], 1);
-    }
+    for (int s = 0; s < kAStages; ++s) mbar_init(&ctrl->aready[s], kDeqWarps / 2);
     for (int b = 0; b < C::TBUF; ++b) {
       mbar_init(&ctrl->tfull[b], 1);
       mbar_init(&ctrl->tempty[b], kEpiWarps);
@@ -271,49 +276,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
         const TileAt t = find(tile);
-        constexpr int QL = (BM / 4 + 31) / 32;  // row quads per lane
-        int4 quad[QL];
-        if (g.rows) {
-#pragma unroll
-          for (int i = 0; i < QL; ++i) {
-            int v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int r = (i * 32 + lane) * 4 + j;
-              v[j] = (int)g.a_rows;  // out of range: zeros
-              if (r < t.cnt) {
-                const int src = g.rows[t.row0 + r];
-                if (src >= 0 && src < g.a_rows) v[j] = src;
-              }
-            }
-            quad[i] = make_int4(v[0], v[1], v[2], v[3]);
-          }
-        }
         for (int ks = 0; ks < kstages; ++ks) {
-          if (!mbar_wait(&ctrl->empty[p.i], p.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_TMA)) ok = false;
+          ok = mbar_wait(&ctrl->empty[p.i], p.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_TMA);
           if (__any_sync(0xFFFFFFFFu, !ok)) {
             ok = false;
             break;
           }
-          uint8_t* st = stage_ptr(p.i);
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&ctrl->full[p.i], C::STAGE);
+          if (elect_one()) {
+            uint8_t* st = stage_ptr(p.i);
+            mbar_arrive_expect_tx(&ctrl->full[p.i], g.rows ? kRaw : C::STAGE);
             tma_load_2d(st + BM * 128, &tm_q, &ctrl->full[p.i], ks * (kKs / 2), t.e * g.n + t.n0);
             if (!g.rows) tma_load_2d(st, &tm_a, &ctrl->full[p.i], ks * kKs, t.row0);
           }
           __syncwarp();
-          if (g.rows) {
-#pragma unroll
-            for (int i = 0; i < QL; ++i)
-              if (i * 32 + lane < BM / 4)
-                tma_gather4(st + (size_t)(i * 32 + lane) * 512, &tm_a, &ctrl->full[p.i], ks * kKs, quad[i]);
-          }
           ++it;
           p.next(stages);
         }
       }
       // copies of the last stages must have landed before the CTA may exit
-      if (lane == 0) {
+      if (!ok && lane == 0) {
         const uint32_t n = (uint32_t)stages;
         for (uint32_t j = it > n ? it - n : 0u; j < it; ++j)
           if (!wait_drain(&ctrl->full[j % n], (j / n) & 1u)) break;
@@ -321,56 +302,139 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA
-      if (lane == 0) {
-        Pos p, ap, tp;
-        constexpr uint32_t idesc = idesc_bf16(kBn, BM);
-        constexpr int STEPS = G / 16;  // MMAs per group
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-          int step = 0;
-          for (int ks = 0; ks < kstages; ++ks) {
-            if (!mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA)) goto mma_done;
-            if (!mbar_wait(&ctrl->aready[ap.i], ap.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA)) goto mma_done;
-            tc_fence_after();
-            const uint32_t b_base = smem_u32(stage_ptr(p.i));
-            const uint32_t a_base = tmem + kColA + (uint32_t)ap.i * 32u;
+      Pos p, ap, tp;
+      bool ok = true;
+      constexpr uint32_t idesc = idesc_bf16(kBn, BM);
+      const uint64_t b_desc0 = smem_desc_k_sw128(smem_u32(smem));
+      // MMAs [j0, j1) of a stage (16 elements of K each) into the current
+      // buffer, onto what it holds if `acc`
+      auto mmas = [&](int j0, int j1, uint32_t acc) {
+        const uint64_t b = b_desc0 + (uint64_t)(p.i * (C::STAGE >> 4));
+        const uint32_t a = tmem + kColA + (uint32_t)ap.i * 32u;
+        const uint32_t d = tmem + (uint32_t)(tp.i * BM);
+        if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (ks * kKs + j * 16 >= g.k) break;
-              if (step == 0) {
-                if (!mbar_wait(&ctrl->tempty[tp.i], tp.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_MMA))
-                  goto mma_done;
-                tc_fence_after();
-              }
-              mma_ts(tmem + (uint32_t)(tp.i * BM), a_base + (uint32_t)j * 8u, smem_desc_k_sw128(b_base + j * 32), idesc,
-                     step > 0);
-              if (++step == STEPS) {
-                tc_commit(&ctrl->tfull[tp.i]);
-                tp.next(C::TBUF);
-                step = 0;
-              }
+          for (int j = 0; j < 4; ++j)
+            if (j >= j0 && j < j1) mma_ts(d, a + (uint32_t)j * 8u, b + (uint64_t)(j * 2), idesc, j > j0 ? 1u : acc);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc_commit(bar);
+        __syncwarp();
+      };
+      auto buffer_wait = [&]() {
+        const bool in = mbar_wait(&ctrl->tempty[tp.i], tp.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_MMA);
+        tc_fence_after();
+        return !__any_sync(0xFFFFFFFFu, !in);
+      };
+      auto buffer_done = [&]() {
+        commit(&ctrl->tfull[tp.i]);
+        tp.next(C::TBUF);
+      };
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        for (int ks = 0; ks < kstages; ++ks) {
+          ok = mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA) &&
+               mbar_wait(&ctrl->aready[ap.i], ap.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA);
+          ok = !__any_sync(0xFFFFFFFFu, !ok);
+          if (!ok) break;
+          tc_fence_after();
+          if constexpr (G == 32) {
+            if (!(ok = buffer_wait())) break;
+            mmas(0, 2, 0u);
+            buffer_done();
+            if (ks * kKs + 32 < g.k) {
+              if (!(ok = buffer_wait())) break;
+              mmas(2, 4, 0u);
+              buffer_done();
             }
-            tc_commit(&ctrl->empty[p.i]);
-            tc_commit(&ctrl->afree[ap.i]);
-            p.next(stages);
-            ap.next(kAStages);
+          } else if constexpr (G == 64) {
+            if (!(ok = buffer_wait())) break;
+            mmas(0, 4, 0u);
+            buffer_done();
+          } else {
+            if ((ks & 1) == 0 && !(ok = buffer_wait())) break;
+            mmas(0, 4, (uint32_t)(ks & 1));
+            if (ks & 1) buffer_done();
+          }
+          commit(&ctrl->empty[p.i]);
+          p.next(stages);
+          ap.next(kAStages);
+        }
+      }
+      // every MMA issued so far has completed once this commit arrives
+      commit(&ctrl->drain);
+      wait_drain(&ctrl->drain, 0u);
+      __syncwarp();
+    } else if (g.rows) {
+      // ------------------------------------------------------------ gathered rows
+      // 8 lanes per row, 16 bytes each; the writes are made visible to the
+      // tensor core's reads (async proxy) by the writer before it arrives.
+      const int w = warp - 2;
+      Pos p, dp;
+      uint32_t issued = 0, done = 0;
+      bool ok = true;
+      auto arrive = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->full[dp.i]);
+        dp.next(stages);
+        ++done;
+      };
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        const TileAt t = find(tile);
+        int* idx = s_rows + (w * (BM / 2));
+        __syncwarp();
+        for (int i = lane; i < BM / 2; i += 32) {  // this warp's rows: 4-row quads, alternating
+          const int r = (i >> 2) * 8 + w * 4 + (i & 3);
+          int src = -1;
+          if (r < t.cnt) {
+            src = g.rows[t.row0 + r];
+            if (src >= g.a_rows) src = -1;
+          }
+          idx[i] = src;
+        }
+        __syncwarp();
+        for (int ks = 0; ks < kstages; ++ks) {
+          ok = mbar_wait(&ctrl->empty[p.i], p.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_TMA);
+          if (__any_sync(0xFFFFFFFFu, !ok)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = smem_u32(stage_ptr(p.i));
+          const int c = lane & 7;
+          const bool k_in = ks * kKs + c * 8 < g.k;
+          const uint16_t* src0 = g.a + ks * kKs + c * 8;
+#pragma unroll 6
+          for (int i = lane >> 3; i < BM / 2; i += 4) {
+            const int r = (i >> 2) * 8 + w * 4 + (i & 3);
+            const int src = idx[i];
+            const bool in = k_in && src >= 0;
+            cp_async16(st + (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)), in ? src0 + (size_t)src * (size_t)g.k : g.a, in);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          ++issued;
+          p.next(stages);
+          if (issued - done > (uint32_t)kGatherAhead) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kGatherAhead) : "memory");
+            arrive();
           }
         }
-      mma_done:
-        // every MMA issued so far has completed once this commit arrives
-        tc_commit(&ctrl->drain);
-        wait_drain(&ctrl->drain, 0u);
       }
-      __syncwarp();
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      while (done < issued) arrive();
     }
   } else if (warp < kEpiWarp0) {
     setmaxnreg_dec<kDeqRegs>();
     // ------------------------------------------------------------------ unpack
-    const int q = warp & 3, hk = (warp - kDeqWarp0) >> 2;
+    // two sets of four warps take alternate stages
+    const int q = warp & 3, set = (warp - kDeqWarp0) >> 2;
     const int row = q * 32 + lane;
-    // 16-byte half hk of the row's 32 bytes, 32-byte swizzle
-    const uint32_t roff = (uint32_t)(BM * 128 + row * 32 + ((hk ^ ((row >> 2) & 1)) * 16));
-    const uint32_t t_addr = tmem + ((uint32_t)(q * 32) << 16) + kColA + (uint32_t)hk * 16u;
-    Pos p, ap;
+    // the row's 32 bytes: 16-byte halves exchanged by the 32-byte swizzle
+    const uint32_t roff = (uint32_t)(BM * 128 + row * 32), rsw = (uint32_t)((row >> 2) & 1) * 16u;
+    const uint32_t t_addr = tmem + ((uint32_t)(q * 32) << 16) + kColA;
+    Pos p, ap, fp;  // stage, operand buffer, the stage whose MMAs free that buffer
+    uint32_t it = 0;
     bool ok = true;
     for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
       const uint8_t* zrow = nullptr;
@@ -378,64 +442,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileAt t = find(tile);
         if (t.n0 + row < g.n) zrow = g.zero + ((size_t)t.e * g.n + t.n0 + row) * (size_t)groups;
       }
-      // zero points of this and the next two stages
+      // zero points of a stage's halves
       auto zero_at = [&](int ks) -> uint32_t {
-        const int gi = (ks * kKs + hk * 32) / G;
-        return zrow && gi < groups ? (uint32_t)zrow[gi] : 8u;
+        const int g0 = ks * kKs / G, g1 = (ks * kKs + 32) / G;
+        const uint32_t a = zrow && g0 < groups ? (uint32_t)zrow[g0] : 8u;
+        const uint32_t b = G == 32 ? (zrow && g1 < groups ? (uint32_t)zrow[g1] : 8u) : a;
+        return a | b << 8;
       };
-      uint32_t z0 = 8, z1 = 8, z2 = 8;
+      // this set's first stage of the tile; zero points two of its stages ahead
+      const int ks0 = (int)((it ^ (uint32_t)set) & 1u);
+      uint32_t z0 = 0x0808u, z1 = 0x0808u;
       if (g.zero) {
-        z0 = zero_at(0);
-        z1 = zero_at(1);
-        z2 = zero_at(2);
+        z0 = zero_at(ks0);
+        z1 = zero_at(ks0 + 2);
       }
-      for (int ks = 0; ks < kstages; ++ks) {
-        uint32_t zc = 0xBE00BE00u;  // -8 / 64
-        if (g.zero) {
-          zc = zero_pair(z0);
-          z0 = z1;
-          z1 = z2;
-          z2 = zero_at(ks + 3);
-        }
-        if (!mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP)) ok = false;
-        if (__any_sync(0xFFFFFFFFu, !ok)) {
-          ok = false;
-          break;
-        }
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(smem_u32(stage_ptr(p.i)) + roff)
-                     : "memory");
-        uint32_t v[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // byte j in both halves: its low nibble in bits 0-3 of the low
-            // half, its high nibble in bits 4-7 of the high half; bits below
-            // 256 read as BF16 are that integer times 2^-133
-            const uint32_t b = __byte_perm(w[i], 0u, j | 0x4040 | (j << 8)) & 0x00F0000Fu;
-            v[i * 4 + j] = fma_bf16x2(b, 0x7D007F00u, zc);
+      for (int ks = 0; ks < kstages; ++ks, ++it) {
+        if (((it ^ (uint32_t)set) & 1u) == 0) {
+          uint32_t zc[2] = {0xBE00BE00u, 0xBE00BE00u};  // -8 / 64
+          if (g.zero) {
+            zc[0] = zero_pair(z0 & 0xFFu);
+            zc[1] = zero_pair(z0 >> 8);
+            z0 = z1;
+            z1 = zero_at(ks + 4);
           }
-        // the codes are in registers: the stage may be refilled as far as
-        // this warp is concerned
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->empty[p.i]);
-        if (!mbar_wait(&ctrl->afree[ap.i], ap.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_PREP)) ok = false;
-        if (__any_sync(0xFFFFFFFFu, !ok)) {
-          ok = false;
-          break;
+          // the operand buffer is free once the MMAs of kAStages stages ago
+          // have completed, which their stage's release says (this set's own
+          // arrival for that stage is long past, and the stage cannot be
+          // released again before this warp reaches it)
+          ok = mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP) &&
+               (it < (uint32_t)kAStages ||
+                mbar_wait(&ctrl->empty[fp.i], fp.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP));
+          if (__any_sync(0xFFFFFFFFu, !ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t raw = smem_u32(stage_ptr(p.i)) + roff;
+          uint32_t w[2][4];
+#pragma unroll
+          for (int hk = 0; hk < 2; ++hk)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[hk][0]), "=r"(w[hk][1]), "=r"(w[hk][2]), "=r"(w[hk][3])
+                         : "r"(raw + ((uint32_t)(hk * 16) ^ rsw))
+                         : "memory");
+#pragma unroll
+          for (int hk = 0; hk < 2; ++hk) {
+            uint32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                // byte j in both halves: its low nibble in bits 0-3 of the low
+                // half, its high nibble in bits 4-7 of the high half; bits
+                // below 256 read as BF16 are that integer times 2^-133
+                const uint32_t b = __byte_perm(w[hk][i], 0u, j | 0x4040 | (j << 8)) & 0x00F0000Fu;
+                v[i * 4 + j] = fma_bf16x2(b, 0x7D007F00u, zc[hk]);
+              }
+            tmem_st_x16(t_addr + (uint32_t)(ap.i * 32 + hk * 16), v);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctrl->aready[ap.i]);
+            mbar_arrive(&ctrl->empty[p.i]);
+          }
         }
-        tc_fence_after();
-        tmem_st_x16(t_addr + (uint32_t)ap.i * 32u, v);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->aready[ap.i]);
         p.next(stages);
         ap.next(kAStages);
+        if (it >= (uint32_t)kAStages) fp.next(stages);
       }
     }
   } else {
@@ -532,13 +607,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int BM>
 size_t smem_bytes(int stages, int experts) {
-  return 1024 + (size_t)stages * Cfg<BM>::STAGE + sizeof(Ctrl) + 2 * sizeof(int) * ((size_t)experts + 1);
+  return 1024 + (size_t)stages * Cfg<BM>::STAGE + sizeof(Ctrl) + 2 * sizeof(int) * ((size_t)experts + 1) + BM * sizeof(int);
 }
 
 template <int BM>
 int stage_count(int experts) {
   int s = kMaxStages;
-  while (s > 2 && smem_bytes<BM>(s, experts) > kSmemMax) --s;
+  while (s > kAStages + 1 && smem_bytes<BM>(s, experts) > kSmemMax) --s;
   return s;
 }
 
