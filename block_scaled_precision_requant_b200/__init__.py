@@ -73,6 +73,7 @@ __all__ = [
     "proj_silu_scratch_bytes",
     "proj_silu",
     "w4g_proj",
+    "w4g_proj_grouped_scratch_bytes",
     "w4g_proj_grouped",
     "MoeRoute",
     "moe_route_scratch_bytes",
@@ -149,7 +150,9 @@ SIGNATURES = [
     ("bsr_proj_silu_scratch_bytes", ctypes.c_size_t, [_I64, _I64]),
     ("bsr_proj_silu", ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
     ("bsr_w4g_proj", ctypes.c_int, [_P, _W, _P, _I64, _I64, _I64, _P]),
-    ("bsr_w4g_proj_grouped", ctypes.c_int, [_P, _I64, _P, _P, _W, _P, _I64, _I64, _I64, _I64, _P]),
+    ("bsr_w4g_proj_grouped_scratch_bytes", ctypes.c_size_t, [_I64, _I64, _I64]),
+    ("bsr_w4g_proj_grouped", ctypes.c_int, [_P, _I64, _P, _P, _W, _P, _I64, _I64, _I64, _I64, _P, ctypes.c_size_t,
+                                            _P]),
     ("bsr_moe_route_scratch_bytes", ctypes.c_size_t, [_I64, _I64]),
     ("bsr_moe_route", ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_uint, _P, _P, _P, _P, _P, _P,
                                      ctypes.c_size_t, _P]),
@@ -869,7 +872,24 @@ def w4g_proj(a, w_q, w_scale, w_zero=None, out=None, stream=None):
     return out
 
 
-def w4g_proj_grouped(a, offsets, w_q, w_scale, w_zero=None, rows=None, out=None, stream=None):
+def w4g_proj_grouped_scratch_bytes(r: int, experts: int, k: int) -> int:
+    """Scratch bytes of :func:`w4g_proj_grouped` with a row index."""
+    return int(lib().bsr_w4g_proj_grouped_scratch_bytes(r, experts, k))
+
+
+def _scratch(scratch, need, like):
+    """(address, bytes) of ``scratch``, allocated when not given."""
+    torch = _torch()
+    if scratch is None:
+        if not need:
+            return None, 0
+        scratch = _empty((need,), torch.uint8, like)
+    elif not scratch.is_cuda or scratch.device != like.device:
+        raise ValueError(f"scratch must be on {like.device}")
+    return scratch.data_ptr(), scratch.numel() * scratch.element_size()
+
+
+def w4g_proj_grouped(a, offsets, w_q, w_scale, w_zero=None, rows=None, out=None, scratch=None, stream=None):
     """:func:`w4g_proj` grouped by expert: output row r with offsets[e] <= r <
     offsets[e + 1] is ``a[rows[r]]`` (``a[r]`` without ``rows``) times expert
     e's weight.  ``offsets`` [E + 1] and ``rows`` [R] int32 on the device, as
@@ -898,6 +918,7 @@ def w4g_proj_grouped(a, offsets, w_q, w_scale, w_zero=None, rows=None, out=None,
                 experts,
                 n,
                 k,
+                *_scratch(scratch, 0 if rows is None else w4g_proj_grouped_scratch_bytes(r, experts, k), a),
                 _stream_ptr(stream),
             )
         )
@@ -1012,11 +1033,6 @@ def w4g_moe_mlp(x, logits, gate, up, down, top_k: int, renormalize: bool = True,
         inner = _dims(gate[0], 3, "gate codes")[1]
         if out is None:
             out = _empty((tokens, k), torch.bfloat16, x)
-        need = w4g_moe_mlp_scratch_bytes(tokens, experts, top_k, inner, k)
-        if scratch is None:
-            scratch = _empty((need,), torch.uint8, x)
-        elif not scratch.is_cuda or scratch.device != x.device:
-            raise ValueError(f"scratch must be on {x.device}")
         _check(
             lib().bsr_w4g_moe_mlp(
                 _dev(x, torch.bfloat16, (tokens, k), "x"),
@@ -1033,8 +1049,7 @@ def w4g_moe_mlp(x, logits, gate, up, down, top_k: int, renormalize: bool = True,
                 1 if renormalize else 0,
                 inner,
                 k,
-                scratch.data_ptr(),
-                scratch.numel() * scratch.element_size(),
+                *_scratch(scratch, w4g_moe_mlp_scratch_bytes(tokens, experts, top_k, inner, k), x),
                 _stream_ptr(stream),
             )
         )

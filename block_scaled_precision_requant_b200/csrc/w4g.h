@@ -40,11 +40,15 @@ cudaError_t launch_w4g_gemv(const CUtensorMap& tm_q, const W4gArgs& g, const W4g
 // Many rows per expert: the tcgen05 tensor cores, tiles of 128 weight rows x
 // bm activation rows.  Tensor maps: codes [experts * N, K/2] bytes, box 128
 // rows x 32 bytes, 32-byte swizzle; activations [a_rows, K] BF16, box bm rows
-// x 64, 128-byte swizzle (unused with a row index).
+// x 64, 128-byte swizzle.  Takes no row index.
 struct W4gGemmPlan {
   int bm, grid;
 };
 W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms);
+// out[r] = a[rows[r]] for r < *last (clamped to [0, rows_max]); zeros where the
+// index is outside a.  16-byte aligned rows.
+cudaError_t launch_w4g_gather(const uint16_t* a, long long a_rows, const int32_t* rows, const int32_t* last,
+                              uint16_t* out, long long rows_max, int k, cudaStream_t stream, int num_sms);
 cudaError_t launch_w4g_gemm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,
                             int* status, cudaStream_t stream);
 

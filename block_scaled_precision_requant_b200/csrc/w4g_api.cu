@@ -136,27 +136,40 @@ bsr_status encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, u
   return BSR_OK;
 }
 
-bsr_status run_product(const bsr::W4gArgs& g, void* stream) {
-  Device d;
-  bsr_status st = device(d);
-  if (st != BSR_OK) return st;
-  if (g.rows_max <= 16LL * g.experts && g.rows_max <= 4096) {
-    const bsr::W4gGemvPlan p = bsr::w4g_gemv_plan(g, d.num_sms);
-    CUtensorMap tm;
-    if ((st = encode_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, (uint64_t)g.k / 2, (uint64_t)g.experts * g.n,
-                        (uint64_t)g.k / 2, 128, (uint32_t)p.tr, CU_TENSOR_MAP_SWIZZLE_128B, "w4g codes")) != BSR_OK)
-      return st;
-    return cuda_status(bsr::launch_w4g_gemv(tm, g, p, d.status, as_stream(stream)), "w4g projection launch");
+// Few rows per expert: the decode kernel, which reads the weight once for up to
+// 16 rows; else the tensor-core kernel.
+bool few_rows(int64_t r, int64_t experts) { return r <= 16 * experts && r <= 4096; }
+
+// One product, every check and tensor map made before its launch.
+struct Product {
+  bsr::W4gArgs g;
+  bool few = false;
+  bsr::W4gGemvPlan gemv;
+  bsr::W4gGemmPlan gemm;
+  CUtensorMap q, a;
+};
+
+bsr_status plan_product(Product& p, const bsr::W4gArgs& g, const Device& d) {
+  p.g = g;
+  p.few = few_rows(g.rows_max, g.experts);
+  const uint64_t wrows = (uint64_t)g.experts * (uint64_t)g.n, wpitch = (uint64_t)g.k / 2;
+  if (p.few) {
+    p.gemv = bsr::w4g_gemv_plan(g, d.num_sms);
+    return encode_2d(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, wpitch, wrows, wpitch, 128, (uint32_t)p.gemv.tr,
+                     CU_TENSOR_MAP_SWIZZLE_128B, "w4g codes");
   }
-  const bsr::W4gGemmPlan p = bsr::w4g_gemm_plan(g, d.num_sms);
-  CUtensorMap tm_q, tm_a;
-  if ((st = encode_2d(&tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, (uint64_t)g.k / 2, (uint64_t)g.experts * g.n,
-                      (uint64_t)g.k / 2, 32, 128, CU_TENSOR_MAP_SWIZZLE_32B, "w4g codes")) != BSR_OK ||
-      (st = encode_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.a, (uint64_t)g.k, (uint64_t)g.a_rows,
-                      (uint64_t)g.k * 2, 64, (uint32_t)p.bm, CU_TENSOR_MAP_SWIZZLE_128B,
-                      "w4g activations")) != BSR_OK)
-    return st;
-  return cuda_status(bsr::launch_w4g_gemm(tm_q, tm_a, g, p, d.status, as_stream(stream)), "w4g projection launch");
+  p.gemm = bsr::w4g_gemm_plan(g, d.num_sms);
+  const bsr_status st = encode_2d(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, wpitch, wrows, wpitch, 32, 128,
+                                  CU_TENSOR_MAP_SWIZZLE_32B, "w4g codes");
+  if (st != BSR_OK) return st;
+  return encode_2d(&p.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.a, (uint64_t)g.k, (uint64_t)g.a_rows, (uint64_t)g.k * 2,
+                   64, (uint32_t)p.gemm.bm, CU_TENSOR_MAP_SWIZZLE_128B, "w4g activations");
+}
+
+bsr_status run_product(const Product& p, const Device& d, void* stream) {
+  return cuda_status(p.few ? bsr::launch_w4g_gemv(p.q, p.g, p.gemv, d.status, as_stream(stream))
+                           : bsr::launch_w4g_gemm(p.q, p.a, p.g, p.gemm, d.status, as_stream(stream)),
+                     "w4g projection launch");
 }
 
 bsr_status check_route_dims(const char* who, int64_t tokens, int64_t experts, int64_t top_k) {
@@ -179,10 +192,10 @@ bsr_status check_logits(const char* who, const void* logits, int logits_type, un
   return BSR_OK;
 }
 
-// Scratch of the expert MLP: the route's results and scratch, then the gate,
-// up, hidden (their SiLU product) and down rows.
+// Scratch of the expert MLP: the route's results and scratch, the gathered rows,
+// then the gate, up, hidden (their SiLU product) and down rows.
 struct MlpLayout {
-  size_t ids, weights, offsets, rows, pos, route, gate, up, hidden, down, total;
+  size_t ids, weights, offsets, rows, pos, route, ordered, gate, up, hidden, down, total;
 };
 MlpLayout mlp_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner, int64_t k) {
   const size_t pairs = (size_t)tokens * (size_t)top_k;
@@ -199,6 +212,7 @@ MlpLayout mlp_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t inn
   L.rows = take(pairs * 4);
   L.pos = take(pairs * 4);
   L.route = take(bsr::route_scratch_bytes(tokens, (int)experts));
+  L.ordered = take(few_rows((int64_t)pairs, experts) ? 0 : pairs * (size_t)k * 2);
   L.gate = take(pairs * (size_t)inner * 2);
   L.up = take(pairs * (size_t)inner * 2);
   L.hidden = take(pairs * (size_t)inner * 2);
@@ -223,12 +237,23 @@ bsr_status bsr_w4g_proj(const uint16_t* a, const bsr_w4g_weight* w, uint16_t* ou
   if ((st = check_weight(w, "bsr_w4g_proj")) != BSR_OK) return st;
   if (!aligned(a, 16) || !aligned(out, 2))
     return report(BSR_EALIGN, "bsr_w4g_proj: a must be 16-byte aligned, out 2-byte aligned");
-  return run_product(make_args(a, m, nullptr, nullptr, w, out, m, 1, n, k), stream);
+  Device d;
+  Product p;
+  if ((st = device(d)) != BSR_OK) return st;
+  if ((st = plan_product(p, make_args(a, m, nullptr, nullptr, w, out, m, 1, n, k), d)) != BSR_OK) return st;
+  return run_product(p, d, stream);
+}
+
+size_t bsr_w4g_proj_grouped_scratch_bytes(int64_t r, int64_t experts, int64_t k) {
+  if (r <= 0 || !dim_ok(r) || experts < 1 || experts > bsr::kRouteMaxExperts || k <= 0 || !dim_ok(k) ||
+      few_rows(r, experts))
+    return 0;
+  return align256((size_t)r * (size_t)k * 2);
 }
 
 bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t* offsets, const int32_t* rows,
                                 const bsr_w4g_weight* w, uint16_t* out, int64_t r, int64_t experts, int64_t n,
-                                int64_t k, void* stream) {
+                                int64_t k, void* scratch, size_t scratch_bytes, void* stream) {
   bsr_status st = check_format(w, "bsr_w4g_proj_grouped", k);
   if (st != BSR_OK) return st;
   if (!dim_ok(a_rows) || !dim_ok(r) || !dim_ok(n) || !dim_ok(k) || experts < 1 || experts > bsr::kRouteMaxExperts ||
@@ -246,7 +271,25 @@ bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t
   if ((st = check_weight(w, "bsr_w4g_proj_grouped")) != BSR_OK) return st;
   if (!aligned(a, 16) || !aligned(out, 2) || !aligned(offsets, 4) || !aligned(rows, 4))
     return report(BSR_EALIGN, "bsr_w4g_proj_grouped: a must be 16-byte aligned, offsets and rows 4-byte, out 2-byte");
-  return run_product(make_args(a, a_rows, offsets, rows, w, out, r, experts, n, k), stream);
+  // the tensor-core kernel takes its rows in order: gather them first
+  const size_t need = rows ? bsr_w4g_proj_grouped_scratch_bytes(r, experts, k) : 0;
+  if (need && (!scratch || scratch_bytes < need))
+    return report(BSR_ESCRATCH, "scratch of %zu bytes needed, %zu given", need, scratch ? scratch_bytes : (size_t)0);
+  if (need && !aligned(scratch, 256)) return report(BSR_EALIGN, "scratch must be 256-byte aligned");
+  Device d;
+  Product p;
+  if ((st = device(d)) != BSR_OK) return st;
+  uint16_t* ordered = static_cast<uint16_t*>(scratch);
+  if ((st = plan_product(p,
+                         need ? make_args(ordered, r, offsets, nullptr, w, out, r, experts, n, k)
+                              : make_args(a, a_rows, offsets, rows, w, out, r, experts, n, k),
+                         d)) != BSR_OK)
+    return st;
+  if (need && (st = cuda_status(bsr::launch_w4g_gather(a, a_rows, rows, offsets + experts, ordered, r, (int)k,
+                                                       as_stream(stream), d.num_sms),
+                                "row gather launch")) != BSR_OK)
+    return st;
+  return run_product(p, d, stream);
 }
 
 size_t bsr_moe_route_scratch_bytes(int64_t tokens, int64_t experts) {
@@ -343,18 +386,30 @@ bsr_status bsr_w4g_moe_mlp(const uint16_t* x, const void* logits, int logits_typ
   uint16_t* u = reinterpret_cast<uint16_t*>(s + L.up);
   uint16_t* h = reinterpret_cast<uint16_t*>(s + L.hidden);
   uint16_t* y = reinterpret_cast<uint16_t*>(s + L.down);
+  // one gather serves gate and up
+  const bool gather = !few_rows(pairs, experts);
+  uint16_t* ordered = reinterpret_cast<uint16_t*>(s + L.ordered);
+  const uint16_t* in = gather ? ordered : x;
+  const int64_t in_rows = gather ? pairs : tokens;
+  const int32_t* in_idx = gather ? nullptr : rows;
+  Product pg, pu, pd;
+  if ((st = plan_product(pg, make_args(in, in_rows, offsets, in_idx, gate, g, pairs, experts, inner, k), d)) !=
+          BSR_OK ||
+      (st = plan_product(pu, make_args(in, in_rows, offsets, in_idx, up, u, pairs, experts, inner, k), d)) != BSR_OK ||
+      (st = plan_product(pd, make_args(h, pairs, offsets, nullptr, down, y, pairs, experts, k, inner), d)) != BSR_OK)
+    return st;
   if ((st = bsr_moe_route(logits, logits_type, tokens, experts, top_k, flags, ids, weights, offsets, rows, pos,
-                          s + L.route, L.gate - L.route, stream)) != BSR_OK)
+                          s + L.route, L.ordered - L.route, stream)) != BSR_OK)
     return st;
-  if ((st = run_product(make_args(x, tokens, offsets, rows, gate, g, pairs, experts, inner, k), stream)) != BSR_OK)
+  if (gather && (st = cuda_status(bsr::launch_w4g_gather(x, tokens, rows, offsets + experts, ordered, pairs, (int)k,
+                                                         as_stream(stream), d.num_sms),
+                                  "row gather launch")) != BSR_OK)
     return st;
-  if ((st = run_product(make_args(x, tokens, offsets, rows, up, u, pairs, experts, inner, k), stream)) != BSR_OK)
-    return st;
+  if ((st = run_product(pg, d, stream)) != BSR_OK || (st = run_product(pu, d, stream)) != BSR_OK) return st;
   if ((st = cuda_status(bsr::launch_silu_mul(g, u, h, (int)pairs, (int)inner, as_stream(stream), d.num_sms),
                         "silu_mul launch")) != BSR_OK)
     return st;
-  if ((st = run_product(make_args(h, pairs, offsets, nullptr, down, y, pairs, experts, k, inner), stream)) != BSR_OK)
-    return st;
+  if ((st = run_product(pd, d, stream)) != BSR_OK) return st;
   return bsr_moe_combine(y, pairs, pos, weights, residual, out, tokens, top_k, k, stream);
 }
 

@@ -12,9 +12,11 @@
 // instructions per 8 elements) and store them with tcgen05.st as the A operand of `tcgen05.mma kind::f16`.
 // Through shared memory the unpacked tile (16 KB per stage, written once and
 // read once) would compete with the activation tile for its bandwidth.
-// Activations (B operand) come by TMA into 128-byte-swizzled tiles; the rows
-// of a gathered tile by 16-byte asynchronous copies of two warps (TMA's
-// four-row gathers took 73 cycles each to issue, 32 and more per stage).
+// Activations (B operand) come by TMA into 128-byte-swizzled tiles, so a row
+// index is resolved by a copy of the rows beforehand (w4g_gather_kernel): the
+// tile's rows gathered here measured 454 (TMA four-row gathers) and 284
+// (16-byte asynchronous copies of two warps) against 1040 TFLOP/s for tile
+// loads, while the copy is 2% of a product of 14336 weight rows.
 //
 // The scale changes every G elements of K, so each group accumulates into its
 // own tensor-memory buffer (a ring of 384 / BM) and the epilogue adds s * P
@@ -28,7 +30,7 @@
 // same weight tile), from offsets read on the device.
 //
 // Warps (20): 0 TMA loads, 1 MMAs (one elected lane; owns the tensor memory),
-// 2-3 gathered rows, 4-11 unpack (warp w: lanes 32 (w % 4)..), 12-19 epilogue (lanes 32 (w % 4).., column half).  Every wait is bounded: a
+// 2-3 idle, 4-11 unpack (warp w: lanes 32 (w % 4)..), 12-19 epilogue (lanes 32 (w % 4).., column half).  Every wait is bounded: a
 // wait that runs out sets a status bit and every role leaves its loop; copies
 // and MMAs in flight are drained (bounded) before the tensor memory is freed.
 #include <cuda_bf16.h>
@@ -47,8 +49,7 @@ constexpr int kKs = 64;        // elements of K per stage
 constexpr int kRaw = kBn * kKs / 2;
 constexpr int kThreads = 640;
 constexpr int kDeqWarp0 = 4, kEpiWarp0 = 12;
-constexpr int kDeqWarps = 8, kEpiWarps = 8, kGatherWarps = 2;
-constexpr int kGatherAhead = 3;  // stages of a gather warp in flight
+constexpr int kDeqWarps = 8, kEpiWarps = 8;
 constexpr int kAStages = 4;    // unpacked stages in tensor memory, 32 columns each
 constexpr uint32_t kColA = 384, kTmemCols = 512;
 constexpr int kMaxStages = 12;
@@ -60,7 +61,11 @@ static_assert(128 * kCtrlRegs + 256 * kDeqRegs + 256 * kEpiRegs <= kThreads * kL
 template <int BM>
 struct Cfg {
   static constexpr int TBUF = 384 / BM < 6 ? 384 / BM : 6;
-  static constexpr int COLS = BM / 2;                 // columns per epilogue warp
+  static constexpr int COLS = BM / 2;                     // columns per epilogue warp
+  static constexpr int CW = BM == 192 || BM == 32 ? 16 : 32;  // per tensor-memory load
+  static constexpr int CH = COLS / CW;
+  // loads of a buffer in flight at once: all where the registers allow
+  static constexpr int AHEAD = BM == 192 ? 2 : CH;
   static constexpr int STAGE = kRaw + BM * 128;
 };
 
@@ -103,12 +108,23 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
 
 // Ties registers written by a tensor-memory load to this point of the
 // program (after tcgen05.wait::ld).
-__device__ __forceinline__ void regs_after_wait(uint32_t (&r)[16]) {
+template <int R>
+__device__ __forceinline__ void regs_after_wait(uint32_t (&r)[R]) {
 #pragma unroll
-  for (int i = 0; i < 16; i += 8)
+  for (int i = 0; i < R; i += 8)
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                       "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
@@ -144,11 +160,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// 16 bytes global -> shared, zeros if !in.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-
 struct TileAt {
   int e, n0, row0, cnt;
 };
@@ -175,7 +186,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + (size_t)stages * C::STAGE);
   int* s_off = reinterpret_cast<int*>(ctrl + 1);
   int* s_pre = s_off + g.experts + 1;
-  int* s_rows = s_pre + g.experts + 1;  // [BM], of the gather warps
   volatile int* abort_flag = &ctrl->abort_flag;
   // through a shuffle, so that the compiler knows it uniform: the roles' loops
   // then keep their descriptors and addresses in uniform registers
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(&ctrl->full[s], g.rows ? 1 + kGatherWarps : 1);
+      mbar_init(&ctrl->full[s], 1);
       mbar_init(&ctrl->empty[s], 1 + kDeqWarps / 2);  // the MMA commit + the stage's unpacking warps
     }
     for (int s = 0; s < kAStages; ++s) mbar_init(&ctrl->aready[s], kDeqWarps / 2);
@@ -284,9 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (elect_one()) {
             uint8_t* st = stage_ptr(p.i);
-            mbar_arrive_expect_tx(&ctrl->full[p.i], g.rows ? kRaw : C::STAGE);
+            mbar_arrive_expect_tx(&ctrl->full[p.i], C::STAGE);
             tma_load_2d(st + BM * 128, &tm_q, &ctrl->full[p.i], ks * (kKs / 2), t.e * g.n + t.n0);
-            if (!g.rows) tma_load_2d(st, &tm_a, &ctrl->full[p.i], ks * kKs, t.row0);
+            tma_load_2d(st, &tm_a, &ctrl->full[p.i], ks * kKs, t.row0);
           }
           __syncwarp();
           ++it;
@@ -366,63 +376,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit(&ctrl->drain);
       wait_drain(&ctrl->drain, 0u);
       __syncwarp();
-    } else if (g.rows) {
-      // ------------------------------------------------------------ gathered rows
-      // 8 lanes per row, 16 bytes each; the writes are made visible to the
-      // tensor core's reads (async proxy) by the writer before it arrives.
-      const int w = warp - 2;
-      Pos p, dp;
-      uint32_t issued = 0, done = 0;
-      bool ok = true;
-      auto arrive = [&]() {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->full[dp.i]);
-        dp.next(stages);
-        ++done;
-      };
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        const TileAt t = find(tile);
-        int* idx = s_rows + (w * (BM / 2));
-        __syncwarp();
-        for (int i = lane; i < BM / 2; i += 32) {  // this warp's rows: 4-row quads, alternating
-          const int r = (i >> 2) * 8 + w * 4 + (i & 3);
-          int src = -1;
-          if (r < t.cnt) {
-            src = g.rows[t.row0 + r];
-            if (src >= g.a_rows) src = -1;
-          }
-          idx[i] = src;
-        }
-        __syncwarp();
-        for (int ks = 0; ks < kstages; ++ks) {
-          ok = mbar_wait(&ctrl->empty[p.i], p.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_TMA);
-          if (__any_sync(0xFFFFFFFFu, !ok)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = smem_u32(stage_ptr(p.i));
-          const int c = lane & 7;
-          const bool k_in = ks * kKs + c * 8 < g.k;
-          const uint16_t* src0 = g.a + ks * kKs + c * 8;
-#pragma unroll 6
-          for (int i = lane >> 3; i < BM / 2; i += 4) {
-            const int r = (i >> 2) * 8 + w * 4 + (i & 3);
-            const int src = idx[i];
-            const bool in = k_in && src >= 0;
-            cp_async16(st + (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)), in ? src0 + (size_t)src * (size_t)g.k : g.a, in);
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          ++issued;
-          p.next(stages);
-          if (issued - done > (uint32_t)kGatherAhead) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kGatherAhead) : "memory");
-            arrive();
-          }
-        }
-      }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      while (done < issued) arrive();
     }
   } else if (warp < kEpiWarp0) {
     setmaxnreg_dec<kDeqRegs>();
@@ -518,9 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * C::COLS);
-    constexpr int CH = C::COLS / 16;  // 16-column chunks
-    static_assert(C::COLS % 16 == 0, "whole chunks");
-    float2 acc[CH][8];
+    constexpr int CH = C::CH, CW = C::CW, AHEAD = C::AHEAD;
+    static_assert(C::COLS % CW == 0, "whole chunks");
+    float2 acc[CH][CW / 2];
     Pos tp;
     bool ok = true;
     // scales of the next four groups of this thread's weight row
@@ -542,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[c][j] = make_float2(0.0f, 0.0f);
+        for (int j = 0; j < CW / 2; ++j) acc[c][j] = make_float2(0.0f, 0.0f);
       for (int gi = 0; gi < groups; ++gi) {
         const float2 s2 = make_float2(sq[0], sq[0]);
         sq[0] = sq[1];
@@ -556,23 +509,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t tb = tl + (uint32_t)(tp.i * BM);
-        uint32_t r[2][16];
-        tmem_ld(tb, r[0]);
+        uint32_t r[AHEAD][CW];
+        if constexpr (AHEAD == CH) {
+#pragma unroll
+          for (int c = 0; c < CH; ++c) tmem_ld(tb + (uint32_t)(CW * c), r[c]);
+          tc_wait_ld();
+#pragma unroll
+          for (int c = 0; c < CH; ++c) regs_after_wait(r[c]);
+          // the buffer is in registers: hand it back to the MMA
+          tc_fence_before();
+          mbar_arrive_lane0(&ctrl->tempty[tp.i], lane);
+        } else {
+          tmem_ld(tb, r[0]);
+        }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          tc_wait_ld();
-          regs_after_wait(r[c & 1]);
-          if (c + 1 < CH)
-            tmem_ld(tb + 16u * (c + 1), r[(c + 1) & 1]);
-          else {
-            // the last chunk is in registers: hand the buffer back to the MMA
-            tc_fence_before();
-            mbar_arrive_lane0(&ctrl->tempty[tp.i], lane);
+          if constexpr (AHEAD < CH) {
+            tc_wait_ld();
+            regs_after_wait(r[c % AHEAD]);
+            if (c + 1 < CH) {
+              tmem_ld(tb + (uint32_t)(CW * (c + 1)), r[(c + 1) % AHEAD]);
+            } else {
+              tc_fence_before();
+              mbar_arrive_lane0(&ctrl->tempty[tp.i], lane);
+            }
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[c][j] = __ffma2_rn(make_float2(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1])),
-                                   s2, acc[c][j]);
+          for (int j = 0; j < CW / 2; ++j)
+            acc[c][j] = __ffma2_rn(
+                make_float2(__uint_as_float(r[c % AHEAD][2 * j]), __uint_as_float(r[c % AHEAD][2 * j + 1])), s2,
+                acc[c][j]);
         }
         tp.next(C::TBUF);
       }
@@ -589,9 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int j = 0; j < CW; ++j) {
             const float v = (j & 1) ? acc[c][j >> 1].y : acc[c][j >> 1].x;
-            if (c0 + c * 16 + j < now.cnt) *o = __float2bfloat16_rn(64.0f * v);  // the codes were taken / 64
+            if (c0 + c * CW + j < now.cnt) *o = __float2bfloat16_rn(64.0f * v);  // the codes were taken / 64
             asm volatile("add.s64 %0, %0, %1;" : "+l"(o) : "l"((long long)g.n * 2));
           }
       }
@@ -605,9 +571,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
+// Rows of a, by index, in the order of the groups: 16 bytes per thread.  An
+// index outside a gives a row of zeros; rows past the last group are left.
+__global__ void __launch_bounds__(256) w4g_gather_kernel(const uint4* __restrict__ a, const int32_t* __restrict__ rows,
+                                                         const int32_t* __restrict__ last, uint4* __restrict__ out,
+                                                         int rows_max, int a_rows, int cols) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long items = (long long)min(max(__ldg(last), 0), rows_max) * cols;
+  const long long stride = (long long)gridDim.x * 256;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += 4 * stride) {
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const long long at = i + u * stride;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (at < items) {
+        const int r = (int)(at / cols);
+        const int src = __ldg(rows + r);
+        if (src >= 0 && src < a_rows) v[u] = __ldg(a + (size_t)src * cols + (size_t)(at - (long long)r * cols));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * stride < items) out[i + u * stride] = v[u];
+  }
+}
+
 template <int BM>
 size_t smem_bytes(int stages, int experts) {
-  return 1024 + (size_t)stages * Cfg<BM>::STAGE + sizeof(Ctrl) + 2 * sizeof(int) * ((size_t)experts + 1) + BM * sizeof(int);
+  return 1024 + (size_t)stages * Cfg<BM>::STAGE + sizeof(Ctrl) + 2 * sizeof(int) * ((size_t)experts + 1);
 }
 
 template <int BM>
@@ -672,20 +665,42 @@ W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms) {
   const long long active = g.rows_max < g.experts ? g.rows_max : g.experts;
   const long long n_tiles = (g.n + kBn - 1) / kBn;
   const long long rows = (g.rows_max + active - 1) / active;  // of an expert, on average
+  // Time of a tile by group (128, 64, 32) and width, relative: whole-kernel
+  // times of a 2048 x 14336 x 4096 product divided by its waves of tiles
+  // (100 = 10 us).
   const int widths[4] = {192, 128, 64, 32};
-  double best = 0.0;
-  for (int bm : widths) {
-    const long long tiles = n_tiles * active * ((rows + bm - 1) / bm);
-    const long long waves = (tiles + num_sms - 1) / num_sms;
-    const double cost = (double)waves * (bm < 80 ? 80 : bm);
-    if (best == 0.0 || cost < best - 1e-9) {
+  const int tile_time[3][4] = {{215, 175, 161, 159}, {326, 246, 193, 172}, {513, 424, 338, 291}};
+  const int* time = tile_time[g.group == 128 ? 0 : g.group == 64 ? 1 : 2];
+  long long best = 0;
+  for (int i = 0; i < 4; ++i) {
+    const long long tiles = n_tiles * active * ((rows + widths[i] - 1) / widths[i]);
+    const long long cost = (tiles + num_sms - 1) / num_sms * time[i];
+    if (i == 0 || cost < best) {
       best = cost;
-      p.bm = bm;
+      p.bm = widths[i];
     }
   }
   const long long most = n_tiles * (active + g.rows_max / p.bm);  // of any grouping
   p.grid = (int)(most < num_sms ? most : num_sms);
   return p;
+}
+
+cudaError_t launch_w4g_gather(const uint16_t* a, long long a_rows, const int32_t* rows, const int32_t* last,
+                              uint16_t* out, long long rows_max, int k, cudaStream_t stream, int num_sms) {
+  const int cols = k / 8;
+  const long long blocks = (rows_max * cols + 1023) / 1024;
+  const long long cap = (long long)num_sms * 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks < cap ? blocks : cap));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, w4g_gather_kernel, reinterpret_cast<const uint4*>(a), rows, last,
+                            reinterpret_cast<uint4*>(out), (int)rows_max, (int)a_rows, cols);
 }
 
 cudaError_t launch_w4g_gemm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,

@@ -463,11 +463,15 @@ bsr_status bsr_w4g_proj(const uint16_t* a, const bsr_w4g_weight* w, uint16_t* ou
  * as 0, each later offset is clamped to [the one before, R]; a row index
  * outside [0, a_rows) stands for a row of zeros.  Rows of out at or past
  * offsets[E] are left as they were.  1 <= E <= BSR_MOE_MAX_EXPERTS, E * N
- * below 2^31; shapes and alignment as bsr_w4g_proj.
+ * below 2^31; shapes and alignment as bsr_w4g_proj.  Scratch (device, 256-byte
+ * aligned) of bsr_w4g_proj_grouped_scratch_bytes(R, E, K), which holds the
+ * rows in group order; none is needed (and 0 is returned) for few rows per
+ * expert, nor when rows is NULL.
  */
+size_t bsr_w4g_proj_grouped_scratch_bytes(int64_t r, int64_t experts, int64_t k);
 bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t* offsets, const int32_t* rows,
                                 const bsr_w4g_weight* w, uint16_t* out, int64_t r, int64_t experts, int64_t n,
-                                int64_t k, void* stream);
+                                int64_t k, void* scratch, size_t scratch_bytes, void* stream);
 
 /*
  * bsr_moe_route -- top-k routing and the grouping of its (token, slot) pairs

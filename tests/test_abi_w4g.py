@@ -55,8 +55,8 @@ def test_proj(L):
 
 
 def test_proj_grouped(L):
-    def call(a=A, a_rows=4, off=A, rows=A, w=None, out=A, r=4, e=2, n=8, k=64):
-        return L.bsr_w4g_proj_grouped(a, a_rows, off, rows, w or weight(), out, r, e, n, k, None)
+    def call(a=A, a_rows=4, off=A, rows=A, w=None, out=A, r=4, e=2, n=8, k=64, scratch=None, nbytes=0):
+        return L.bsr_w4g_proj_grouped(a, a_rows, off, rows, w or weight(), out, r, e, n, k, scratch, nbytes, None)
 
     assert call(e=0) == EINVAL and call(e=1025) == EINVAL and call(n=2 ** 30, e=2) == EINVAL
     assert call(r=-1) == EINVAL and call(a_rows=-1) == EINVAL
@@ -65,6 +65,12 @@ def test_proj_grouped(L):
     assert call(off=P(258)) == EALIGN and call(rows=P(258)) == EALIGN and call(a=P(264)) == EALIGN
     assert call(w=weight(q=8)) == EALIGN and call(k=32) == ESHAPE
     assert call(a=None, off=None, rows=None, out=None, r=0) == OK
+    # many rows per expert and a row index: the rows in group order
+    assert L.bsr_w4g_proj_grouped_scratch_bytes(32, 2, 64) == 0
+    need = L.bsr_w4g_proj_grouped_scratch_bytes(33, 2, 64)
+    assert need == (33 * 64 * 2 + 255) // 256 * 256 and L.bsr_w4g_proj_grouped_scratch_bytes(-1, 2, 64) == 0
+    assert call(r=33) == ESCRATCH and call(r=33, scratch=A, nbytes=need - 1) == ESCRATCH
+    assert call(r=33, scratch=P(128), nbytes=need) == EALIGN
 
 
 def test_route(L):
