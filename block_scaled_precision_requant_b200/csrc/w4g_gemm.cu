@@ -62,10 +62,8 @@ template <int BM>
 struct Cfg {
   static constexpr int TBUF = 384 / BM < 6 ? 384 / BM : 6;
   static constexpr int COLS = BM / 2;                     // columns per epilogue warp
-  static constexpr int CW = BM == 192 || BM == 32 ? 16 : 32;  // per tensor-memory load
-  static constexpr int CH = COLS / CW;
-  // loads of a buffer in flight at once: all where the registers allow
-  static constexpr int AHEAD = BM == 192 ? 2 : CH;
+  static constexpr int CH = BM == 192 ? 2 : 1;            // chunks that go through registers at once
+  static constexpr int CW = COLS / CH;                    // columns of a chunk: 48, 64, 32, 16
   static constexpr int STAGE = kRaw + BM * 128;
 };
 
@@ -117,6 +115,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+// CW columns as loads of 32 and 16.
+template <int CW>
+__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[CW]) {
+#pragma unroll
+  for (int i = 0; i + 32 <= CW; i += 32) tmem_ld(taddr + (uint32_t)i, reinterpret_cast<uint32_t(&)[32]>(r[i]));
+  if constexpr (CW % 32 == 16)
+    tmem_ld(taddr + (uint32_t)(CW - 16), reinterpret_cast<uint32_t(&)[16]>(r[CW - 16]));
 }
 
 // Ties registers written by a tensor-memory load to this point of the
@@ -312,13 +319,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA
+      // A stage's unpacked codes are ready only after its activations landed
+      // (the unpacking warps waited for both), so that is the one wait.
       Pos p, ap, tp;
       bool ok = true;
       constexpr uint32_t idesc = idesc_bf16(kBn, BM);
       const uint64_t b_desc0 = smem_desc_k_sw128(smem_u32(smem));
       // MMAs [j0, j1) of a stage (16 elements of K each) into the current
-      // buffer, onto what it holds if `acc`
-      auto mmas = [&](int j0, int j1, uint32_t acc) {
+      // buffer, onto what it holds if `acc`; then, if asked, the buffer's and
+      // the stage's commits
+      auto mmas = [&](int j0, int j1, uint32_t acc, bool buffer, bool stage) {
         const uint64_t b = b_desc0 + (uint64_t)(p.i * (C::STAGE >> 4));
         const uint32_t a = tmem + kColA + (uint32_t)ap.i * 32u;
         const uint32_t d = tmem + (uint32_t)(tp.i * BM);
@@ -326,54 +336,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (j >= j0 && j < j1) mma_ts(d, a + (uint32_t)j * 8u, b + (uint64_t)(j * 2), idesc, j > j0 ? 1u : acc);
+          if (buffer) tc_commit(&ctrl->tfull[tp.i]);
+          if (stage) tc_commit(&ctrl->empty[p.i]);
         }
         __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
+        if (buffer) tp.next(C::TBUF);
       };
       auto buffer_wait = [&]() {
         const bool in = mbar_wait(&ctrl->tempty[tp.i], tp.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_MMA);
-        tc_fence_after();
         return !__any_sync(0xFFFFFFFFu, !in);
-      };
-      auto buffer_done = [&]() {
-        commit(&ctrl->tfull[tp.i]);
-        tp.next(C::TBUF);
       };
       for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
         for (int ks = 0; ks < kstages; ++ks) {
-          ok = mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA) &&
-               mbar_wait(&ctrl->aready[ap.i], ap.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA);
+          if ((G != 128 || (ks & 1) == 0) && !(ok = buffer_wait())) break;
+          ok = mbar_wait(&ctrl->aready[ap.i], ap.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA);
           ok = !__any_sync(0xFFFFFFFFu, !ok);
           if (!ok) break;
           tc_fence_after();
           if constexpr (G == 32) {
-            if (!(ok = buffer_wait())) break;
-            mmas(0, 2, 0u);
-            buffer_done();
-            if (ks * kKs + 32 < g.k) {
+            const bool two = ks * kKs + 32 < g.k;
+            mmas(0, 2, 0u, true, !two);
+            if (two) {
               if (!(ok = buffer_wait())) break;
-              mmas(2, 4, 0u);
-              buffer_done();
+              tc_fence_after();
+              mmas(2, 4, 0u, true, true);
             }
           } else if constexpr (G == 64) {
-            if (!(ok = buffer_wait())) break;
-            mmas(0, 4, 0u);
-            buffer_done();
+            mmas(0, 4, 0u, true, true);
           } else {
-            if ((ks & 1) == 0 && !(ok = buffer_wait())) break;
-            mmas(0, 4, (uint32_t)(ks & 1));
-            if (ks & 1) buffer_done();
+            mmas(0, 4, (uint32_t)(ks & 1), (ks & 1) != 0, true);
           }
-          commit(&ctrl->empty[p.i]);
           p.next(stages);
           ap.next(kAStages);
         }
       }
       // every MMA issued so far has completed once this commit arrives
-      commit(&ctrl->drain);
+      if (elect_one()) tc_commit(&ctrl->drain);
       wait_drain(&ctrl->drain, 0u);
       __syncwarp();
     }
@@ -387,6 +385,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t roff = (uint32_t)(BM * 128 + row * 32), rsw = (uint32_t)((row >> 2) & 1) * 16u;
     const uint32_t t_addr = tmem + ((uint32_t)(q * 32) << 16) + kColA;
     Pos p, ap, fp;  // stage, operand buffer, the stage whose MMAs free that buffer
+    // The set's last stage whose stores are in flight: they are waited for, and
+    // the stage handed on, once the next stage's codes have been read, so that
+    // the stores' latency passes during the reads.
+    int last_stage = -1, last_buf = 0;
+    auto finish = [&]() {
+      if (last_stage < 0) return;
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctrl->aready[last_buf]);
+        mbar_arrive(&ctrl->empty[last_stage]);
+      }
+      last_stage = -1;
+    };
     uint32_t it = 0;
     bool ok = true;
     for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
@@ -395,16 +408,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileAt t = find(tile);
         if (t.n0 + row < g.n) zrow = g.zero + ((size_t)t.e * g.n + t.n0 + row) * (size_t)groups;
       }
-      // zero points of a stage's halves
-      auto zero_at = [&](int ks) -> uint32_t {
+      // zero points of a stage's halves, as stored
+      struct Zeros {
+        uint8_t a, b;
+      };
+      auto zero_at = [&](int ks) {
         const int g0 = ks * kKs / G, g1 = (ks * kKs + 32) / G;
-        const uint32_t a = zrow && g0 < groups ? (uint32_t)zrow[g0] : 8u;
-        const uint32_t b = G == 32 ? (zrow && g1 < groups ? (uint32_t)zrow[g1] : 8u) : a;
-        return a | b << 8;
+        Zeros z = {8, 8};
+        if (zrow && g0 < groups) z.a = __ldg(zrow + g0);
+        if (G == 32 && zrow && g1 < groups) z.b = __ldg(zrow + g1);
+        return z;
       };
       // this set's first stage of the tile; zero points two of its stages ahead
       const int ks0 = (int)((it ^ (uint32_t)set) & 1u);
-      uint32_t z0 = 0x0808u, z1 = 0x0808u;
+      Zeros z0 = {8, 8}, z1 = {8, 8};
       if (g.zero) {
         z0 = zero_at(ks0);
         z1 = zero_at(ks0 + 2);
@@ -413,23 +430,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (((it ^ (uint32_t)set) & 1u) == 0) {
           uint32_t zc[2] = {0xBE00BE00u, 0xBE00BE00u};  // -8 / 64
           if (g.zero) {
-            zc[0] = zero_pair(z0 & 0xFFu);
-            zc[1] = zero_pair(z0 >> 8);
+            zc[0] = zero_pair(z0.a);
+            zc[1] = G == 32 ? zero_pair(z0.b) : zc[0];
             z0 = z1;
             z1 = zero_at(ks + 4);
           }
-          // the operand buffer is free once the MMAs of kAStages stages ago
-          // have completed, which their stage's release says (this set's own
-          // arrival for that stage is long past, and the stage cannot be
-          // released again before this warp reaches it)
-          ok = mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP) &&
-               (it < (uint32_t)kAStages ||
-                mbar_wait(&ctrl->empty[fp.i], fp.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP));
+          ok = mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP);
           if (__any_sync(0xFFFFFFFFu, !ok)) {
             ok = false;
             break;
           }
-          tc_fence_after();
           const uint32_t raw = smem_u32(stage_ptr(p.i)) + roff;
           uint32_t w[2][4];
 #pragma unroll
@@ -438,6 +448,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : "=r"(w[hk][0]), "=r"(w[hk][1]), "=r"(w[hk][2]), "=r"(w[hk][3])
                          : "r"(raw + ((uint32_t)(hk * 16) ^ rsw))
                          : "memory");
+          finish();
+          // the operand buffer is free once the MMAs of kAStages stages ago
+          // have completed, which their stage's release says (this set's own
+          // arrival for that stage is long past, and the stage cannot be
+          // released again before this warp reaches it)
+          if (it >= (uint32_t)kAStages) {
+            ok = mbar_wait(&ctrl->empty[fp.i], fp.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP);
+            if (__any_sync(0xFFFFFFFFu, !ok)) {
+              ok = false;
+              break;
+            }
+          }
+          tc_fence_after();
 #pragma unroll
           for (int hk = 0; hk < 2; ++hk) {
             uint32_t v[16];
@@ -453,33 +476,30 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             tmem_st_x16(t_addr + (uint32_t)(ap.i * 32 + hk * 16), v);
           }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ctrl->aready[ap.i]);
-            mbar_arrive(&ctrl->empty[p.i]);
-          }
+          last_stage = p.i;
+          last_buf = ap.i;
         }
         p.next(stages);
         ap.next(kAStages);
         if (it >= (uint32_t)kAStages) fp.next(stages);
       }
     }
+    finish();
   } else {
     setmaxnreg_inc<kEpiRegs>();
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * C::COLS);
-    constexpr int CH = C::CH, CW = C::CW, AHEAD = C::AHEAD;
-    static_assert(C::COLS % CW == 0, "whole chunks");
+    constexpr int CH = C::CH, CW = C::CW;
+    static_assert(C::COLS == CH * CW && CW % 16 == 0, "whole chunks");
     float2 acc[CH][CW / 2];
     Pos tp;
     bool ok = true;
-    // scales of the next four groups of this thread's weight row
-    float sq[4];
+    // scales of the next four groups of this thread's weight row, as stored (a
+    // conversion here would wait for the load)
+    uint16_t sq[4];
     const uint16_t* srow = nullptr;
-    auto scale_at = [&](int gi) { return srow && gi < groups ? scale_f32(srow[gi], g.half_scale) : 0.0f; };
+    auto scale_at = [&](int gi) -> uint16_t { return srow && gi < groups ? __ldg(srow + gi) : (uint16_t)0; };
     auto open_tile = [&](const TileAt& t) {
       const int n = t.n0 + q * 32 + lane;
       srow = n < g.n ? g.scale + ((size_t)t.e * g.n + n) * (size_t)groups : nullptr;
@@ -497,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < CW / 2; ++j) acc[c][j] = make_float2(0.0f, 0.0f);
       for (int gi = 0; gi < groups; ++gi) {
-        const float2 s2 = make_float2(sq[0], sq[0]);
+        const float sc = scale_f32(sq[0], g.half_scale);
+        const float2 s2 = make_float2(sc, sc);
         sq[0] = sq[1];
         sq[1] = sq[2];
         sq[2] = sq[3];
@@ -509,36 +530,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t tb = tl + (uint32_t)(tp.i * BM);
-        uint32_t r[AHEAD][CW];
-        if constexpr (AHEAD == CH) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) tmem_ld(tb + (uint32_t)(CW * c), r[c]);
-          tc_wait_ld();
-#pragma unroll
-          for (int c = 0; c < CH; ++c) regs_after_wait(r[c]);
-          // the buffer is in registers: hand it back to the MMA
-          tc_fence_before();
-          mbar_arrive_lane0(&ctrl->tempty[tp.i], lane);
-        } else {
-          tmem_ld(tb, r[0]);
-        }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          if constexpr (AHEAD < CH) {
-            tc_wait_ld();
-            regs_after_wait(r[c % AHEAD]);
-            if (c + 1 < CH) {
-              tmem_ld(tb + (uint32_t)(CW * (c + 1)), r[(c + 1) % AHEAD]);
-            } else {
-              tc_fence_before();
-              mbar_arrive_lane0(&ctrl->tempty[tp.i], lane);
-            }
+          uint32_t r[CW];
+          tmem_ld_chunk(tb + (uint32_t)(CW * c), r);
+          tc_wait_ld();
+          regs_after_wait(r);
+          if (c + 1 == CH) {  // the buffer is in registers: hand it back to the MMA
+            tc_fence_before();
+            mbar_arrive_lane0(&ctrl->tempty[tp.i], lane);
           }
 #pragma unroll
           for (int j = 0; j < CW / 2; ++j)
-            acc[c][j] = __ffma2_rn(
-                make_float2(__uint_as_float(r[c % AHEAD][2 * j]), __uint_as_float(r[c % AHEAD][2 * j + 1])), s2,
-                acc[c][j]);
+            acc[c][j] = __ffma2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2, acc[c][j]);
         }
         tp.next(C::TBUF);
       }
