@@ -8,7 +8,7 @@
 // Tile: 128 weight rows (tensor-memory lanes, MMA M) x BM activation rows of
 // one expert (columns, MMA N).  The codes are the A operand and go through
 // tensor memory: a stage's codes (128 rows x 64 elements, 4 KB) come by TMA,
-// two sets of four warps unpack alternate stages to BF16 pairs (12
+// two sets of four warps unpack alternate stages to BF16 pairs (10
 // instructions per 8 elements) and store them with tcgen05.st as the A operand of `tcgen05.mma kind::f16`.
 // Through shared memory the unpacked tile (16 KB per stage, written once and
 // read once) would compete with the activation tile for its bandwidth.
@@ -54,9 +54,7 @@ constexpr int kAStages = 4;    // unpacked stages in tensor memory, 32 columns e
 constexpr uint32_t kColA = 384, kTmemCols = 512;
 constexpr int kMaxStages = 12;
 constexpr size_t kSmemMax = 232448;
-// register split: launched with 96 per thread
-constexpr int kLaunchRegs = 96, kCtrlRegs = 48, kDeqRegs = 48, kEpiRegs = 168;
-static_assert(128 * kCtrlRegs + 256 * kDeqRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kLaunchRegs = 96, kCtrlRegs = 48;
 
 template <int BM>
 struct Cfg {
@@ -65,6 +63,10 @@ struct Cfg {
   static constexpr int CH = BM == 192 ? 2 : 1;            // chunks that go through registers at once
   static constexpr int CW = COLS / CH;                    // columns of a chunk: 48, 64, 32, 16
   static constexpr int STAGE = kRaw + BM * 128;
+  // register split: launched with kLaunchRegs per thread
+  static constexpr int EPI_REGS = BM == 192 ? 168 : 136;
+  static constexpr int DEQ_REGS = BM == 192 ? 48 : 80;
+  static_assert(128 * kCtrlRegs + 256 * (DEQ_REGS + EPI_REGS) <= kThreads * kLaunchRegs, "register split");
 };
 
 struct Ctrl {
@@ -139,6 +141,13 @@ __device__ __forceinline__ void regs_after_wait(uint32_t (&r)[R]) {
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// prmt, whose selectors with bit 3 set give a byte of copies of the sign bit.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
   return d;
 }
 
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp < kEpiWarp0) {
-    setmaxnreg_dec<kDeqRegs>();
+    setmaxnreg_dec<C::DEQ_REGS>();
     // ------------------------------------------------------------------ unpack
     // two sets of four warps take alternate stages
     const int q = warp & 3, set = (warp - kDeqWarp0) >> 2;
@@ -465,15 +474,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int hk = 0; hk < 2; ++hk) {
             uint32_t v[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+              // low and high nibbles of the four bytes; byte j of each makes a
+              // pair of halves (a sign byte of `lo` is zero): the low nibble in
+              // bits 0-3, the high one in bits 4-7.  Bits below 256 read as
+              // BF16 are that integer times 2^-133.
+              const uint32_t lo = w[hk][i] & 0x0F0F0F0Fu, hi = w[hk][i] & 0xF0F0F0F0u;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                // byte j in both halves: its low nibble in bits 0-3 of the low
-                // half, its high nibble in bits 4-7 of the high half; bits
-                // below 256 read as BF16 are that integer times 2^-133
-                const uint32_t b = __byte_perm(w[hk][i], 0u, j | 0x4040 | (j << 8)) & 0x00F0000Fu;
-                v[i * 4 + j] = fma_bf16x2(b, 0x7D007F00u, zc[hk]);
-              }
+              for (int j = 0; j < 4; ++j)
+                v[i * 4 + j] = fma_bf16x2(prmt(lo, hi, 0x8080u | (uint32_t)(j | (4 + j) << 8)), 0x7D007F00u,
+                                          zc[hk]);
+            }
             tmem_st_x16(t_addr + (uint32_t)(ap.i * 32 + hk * 16), v);
           }
           last_stage = p.i;
@@ -486,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     finish();
   } else {
-    setmaxnreg_inc<kEpiRegs>();
+    setmaxnreg_inc<C::EPI_REGS>();
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * C::COLS);
