@@ -800,26 +800,43 @@ def gemm_block_m(m: int, n: int) -> int:
 # ---------------------------------------------------------------------------
 
 
-def _on(t):
-    """A context in which ``t``'s device is the current one (the library
-    launches on the current device, and the default stream is its)."""
+# These entries serve decode steps of a few microseconds, so the checks of a
+# well-formed call are kept to one expression per tensor; what is wrong is
+# worked out only when something is.
+
+
+def _like(t, name):
+    """(device index, context in which it is the current device) of the tensor
+    that fixes a call's device: the library launches on the current device."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index, _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _beside(t, dtype, shape, name, like):
-    """:func:`_dev` of a tensor that must be on ``like``'s device."""
-    p = _dev(t, dtype, shape, name)
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    return p
+_HERE = contextlib.nullcontext()
 
 
-def _w4g_weight(w_q, w_scale, w_zero, lead, n, k, like, name):
+def _ptr(t, dtype, shape, name, index):
+    """The address of a contiguous tensor of this dtype and shape on device
+    ``index``."""
+    try:
+        if t.dtype == dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, shape, name)
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
+def _raw_stream(stream, index):
+    return _torch()._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _w4g_weight(w_q, w_scale, w_zero, lead, n, k, index, name):
     """The bsr_w4g_weight of codes ``lead + (n, k/2)`` uint8, scales ``lead +
     (n, k/G)`` bfloat16 or float16, zero points (or None) like the scales,
     uint8."""
@@ -829,22 +846,35 @@ def _w4g_weight(w_q, w_scale, w_zero, lead, n, k, like, name):
     groups = w_scale.shape[-1]
     if groups == 0 or k % groups or k // groups not in (32, 64, 128):
         raise ValueError(f"{name}: {groups} scales per row of K={k}: the group must be 32, 64 or 128")
-    if w_scale.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"{name} scale must be bfloat16 or float16, got {w_scale.dtype}")
+    kind = w_scale.dtype
+    if kind != torch.bfloat16 and kind != torch.float16:
+        raise TypeError(f"{name} scale must be bfloat16 or float16, got {kind}")
     shape = lead + (n, groups)
     return _W4gWeight(
-        _beside(w_q, torch.uint8, lead + (n, k // 2), f"{name} codes", like).value,
-        _beside(w_scale, w_scale.dtype, shape, f"{name} scale", like).value,
-        None if w_zero is None else _beside(w_zero, torch.uint8, shape, f"{name} zero points", like).value,
-        1 if w_scale.dtype == torch.float16 else 0,
+        _ptr(w_q, torch.uint8, lead + (n, k // 2), f"{name} codes", index),
+        _ptr(w_scale, kind, shape, f"{name} scale", index),
+        None if w_zero is None else _ptr(w_zero, torch.uint8, shape, f"{name} zero points", index),
+        1 if kind == torch.float16 else 0,
         k // groups,
     )
 
 
 def _dims(t, count, name):
-    if t.dim() != count:
-        raise ValueError(f"{name} must have {count} dimensions, got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != count:
+        raise ValueError(f"{name} must have {count} dimensions, got shape {tuple(shape)}")
+    return shape
+
+
+def _scratch(scratch, need, like):
+    """(address, bytes) of ``scratch``, allocated when not given."""
+    if scratch is None:
+        if not need:
+            return None, 0
+        scratch = like.new_empty((need,), dtype=_torch().uint8)
+    elif scratch.get_device() != like.get_device():
+        raise ValueError(f"scratch must be on {like.device}")
+    return scratch.data_ptr(), scratch.numel() * scratch.element_size()
 
 
 def w4g_proj(a, w_q, w_scale, w_zero=None, out=None, stream=None):
@@ -852,41 +882,23 @@ def w4g_proj(a, w_q, w_scale, w_zero=None, out=None, stream=None):
     weight W = (q - zero) * scale: ``w_q`` [N, K/2] uint8 (element 2i in the
     low nibble of byte i), ``w_scale`` [N, K/G] bfloat16 or float16 with G =
     32, 64 or 128, ``w_zero`` [N, K/G] uint8 in 0..15 (None: 8)."""
-    torch = _torch()
-    with _on(a):
-        m, k = _dims(a, 2, "a")
-        n = _dims(w_q, 2, "w_q")[0]
+    bf16 = _torch().bfloat16
+    index, here = _like(a, "a")
+    m, k = _dims(a, 2, "a")
+    n = _dims(w_q, 2, "w_q")[0]
+    a_ptr = _ptr(a, bf16, (m, k), "a", index)
+    w = _w4g_weight(w_q, w_scale, w_zero, (), n, k, index, "w")
+    with here:
         if out is None:
-            out = _empty((m, n), torch.bfloat16, a)
-        _check(
-            lib().bsr_w4g_proj(
-                _dev(a, torch.bfloat16, (m, k), "a"),
-                _w4g_weight(w_q, w_scale, w_zero, (), n, k, a, "w"),
-                _beside(out, torch.bfloat16, (m, n), "out", a),
-                m,
-                n,
-                k,
-                _stream_ptr(stream),
-            )
-        )
+            out = a.new_empty((m, n))
+        _check(lib().bsr_w4g_proj(a_ptr, w, _ptr(out, bf16, (m, n), "out", index), m, n, k,
+                                  _raw_stream(stream, index)))
     return out
 
 
 def w4g_proj_grouped_scratch_bytes(r: int, experts: int, k: int) -> int:
     """Scratch bytes of :func:`w4g_proj_grouped` with a row index."""
-    return int(lib().bsr_w4g_proj_grouped_scratch_bytes(r, experts, k))
-
-
-def _scratch(scratch, need, like):
-    """(address, bytes) of ``scratch``, allocated when not given."""
-    torch = _torch()
-    if scratch is None:
-        if not need:
-            return None, 0
-        scratch = _empty((need,), torch.uint8, like)
-    elif not scratch.is_cuda or scratch.device != like.device:
-        raise ValueError(f"scratch must be on {like.device}")
-    return scratch.data_ptr(), scratch.numel() * scratch.element_size()
+    return lib().bsr_w4g_proj_grouped_scratch_bytes(r, experts, k)
 
 
 def w4g_proj_grouped(a, offsets, w_q, w_scale, w_zero=None, rows=None, out=None, scratch=None, stream=None):
@@ -897,31 +909,21 @@ def w4g_proj_grouped(a, offsets, w_q, w_scale, w_zero=None, rows=None, out=None,
     Returns out [R, N]; rows at or past offsets[E] are left as they were
     (uninitialised when ``out`` is not given)."""
     torch = _torch()
-    with _on(a):
-        a_rows, k = _dims(a, 2, "a")
-        experts, n = _dims(w_q, 3, "w_q")[:2]
-        if rows is None:
-            r = a_rows
-        else:
-            (r,) = _dims(rows, 1, "rows")
+    bf16 = torch.bfloat16
+    index, here = _like(a, "a")
+    a_rows, k = _dims(a, 2, "a")
+    experts, n = _dims(w_q, 3, "w_q")[:2]
+    r = a_rows if rows is None else _dims(rows, 1, "rows")[0]
+    a_ptr = _ptr(a, bf16, (a_rows, k), "a", index)
+    off_ptr = _ptr(offsets, torch.int32, (experts + 1,), "offsets", index)
+    rows_ptr = None if rows is None else _ptr(rows, torch.int32, (r,), "rows", index)
+    w = _w4g_weight(w_q, w_scale, w_zero, (experts,), n, k, index, "w")
+    with here:
         if out is None:
-            out = _empty((r, n), torch.bfloat16, a)
-        _check(
-            lib().bsr_w4g_proj_grouped(
-                _dev(a, torch.bfloat16, (a_rows, k), "a"),
-                a_rows,
-                _beside(offsets, torch.int32, (experts + 1,), "offsets", a),
-                None if rows is None else _beside(rows, torch.int32, (r,), "rows", a),
-                _w4g_weight(w_q, w_scale, w_zero, (experts,), n, k, a, "w"),
-                _beside(out, torch.bfloat16, (r, n), "out", a),
-                r,
-                experts,
-                n,
-                k,
-                *_scratch(scratch, 0 if rows is None else w4g_proj_grouped_scratch_bytes(r, experts, k), a),
-                _stream_ptr(stream),
-            )
-        )
+            out = a.new_empty((r, n))
+        need = 0 if rows is None else lib().bsr_w4g_proj_grouped_scratch_bytes(r, experts, k)
+        _check(lib().bsr_w4g_proj_grouped(a_ptr, a_rows, off_ptr, rows_ptr, w, _ptr(out, bf16, (r, n), "out", index), r,
+                                          experts, n, k, *_scratch(scratch, need, a), _raw_stream(stream, index)))
     return out
 
 
@@ -945,7 +947,7 @@ def _logits_type(logits):
 
 
 def moe_route_scratch_bytes(tokens: int, experts: int) -> int:
-    return int(lib().bsr_moe_route_scratch_bytes(tokens, experts))
+    return lib().bsr_moe_route_scratch_bytes(tokens, experts)
 
 
 def moe_route(logits, top_k: int, renormalize: bool = True, stream=None) -> MoeRoute:
@@ -954,36 +956,26 @@ def moe_route(logits, top_k: int, renormalize: bool = True, stream=None) -> MoeR
     -inf or NaN are masked; ties go to the lowest index; the weights are a
     softmax over the chosen experts (``renormalize``) or over all."""
     torch = _torch()
-    with _on(logits):
-        tokens, experts = _dims(logits, 2, "logits")
-        kind = _logits_type(logits)
-        top_k = int(top_k)
-        if not 1 <= top_k <= experts:
-            raise ValueError(f"top_k must be in 1..{experts}, got {top_k}")
-        need = moe_route_scratch_bytes(tokens, experts)
-        scratch = _empty((need,), torch.uint8, logits) if need else None
-        route = MoeRoute(
-            _empty((tokens, top_k), torch.int32, logits),
-            _empty((tokens, top_k), torch.float32, logits),
-            _empty((experts + 1,), torch.int32, logits),
-            _empty((tokens * top_k,), torch.int32, logits),
-            _empty((tokens, top_k), torch.int32, logits),
-        )
-        _check(
-            lib().bsr_moe_route(
-                _dev(logits, logits.dtype, (tokens, experts), "logits"),
-                kind,
-                tokens,
-                experts,
-                top_k,
-                1 if renormalize else 0,
-                *[t.data_ptr() for t in route],
-                None if scratch is None else scratch.data_ptr(),
-                need,
-                _stream_ptr(stream),
-            )
-        )
-    return route
+    tokens, experts = _dims(logits, 2, "logits")
+    kind = _logits_type(logits)
+    top_k = int(top_k)
+    if not 1 <= top_k <= experts:
+        raise ValueError(f"top_k must be in 1..{experts}, got {top_k}")
+    index, here = _like(logits, "logits")
+    l_ptr = _ptr(logits, logits.dtype, (tokens, experts), "logits", index)
+    with here:
+        need = lib().bsr_moe_route_scratch_bytes(tokens, experts)
+        scratch = logits.new_empty((need,), dtype=torch.uint8) if need else None
+        ids = logits.new_empty((tokens, top_k), dtype=torch.int32)
+        weights = torch.empty_like(ids, dtype=torch.float32)
+        offsets = ids.new_empty((experts + 1,))
+        rows = ids.new_empty((tokens * top_k,))
+        pos = torch.empty_like(ids)
+        _check(lib().bsr_moe_route(l_ptr, kind, tokens, experts, top_k, 1 if renormalize else 0, ids.data_ptr(),
+                                   weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
+                                   None if scratch is None else scratch.data_ptr(), need,
+                                   _raw_stream(stream, index)))
+    return MoeRoute(ids, weights, offsets, rows, pos)
 
 
 def moe_combine(y, pos, weights, residual=None, out=None, stream=None):
@@ -992,30 +984,24 @@ def moe_combine(y, pos, weights, residual=None, out=None, stream=None):
     ``weights`` float32 [T, top_k] as :func:`moe_route` returns them).  A
     position outside [0, R) is skipped.  ``out`` may be ``residual``."""
     torch = _torch()
-    with _on(y):
-        r, n = _dims(y, 2, "y")
-        tokens, top_k = _dims(pos, 2, "pos")
+    bf16 = torch.bfloat16
+    index, here = _like(y, "y")
+    r, n = _dims(y, 2, "y")
+    tokens, top_k = pairs = _dims(pos, 2, "pos")
+    y_ptr = _ptr(y, bf16, (r, n), "y", index)
+    pos_ptr = _ptr(pos, torch.int32, pairs, "pos", index)
+    w_ptr = _ptr(weights, torch.float32, pairs, "weights", index)
+    res_ptr = None if residual is None else _ptr(residual, bf16, (tokens, n), "residual", index)
+    with here:
         if out is None:
-            out = _empty((tokens, n), torch.bfloat16, y)
-        _check(
-            lib().bsr_moe_combine(
-                _dev(y, torch.bfloat16, (r, n), "y"),
-                r,
-                _beside(pos, torch.int32, (tokens, top_k), "pos", y),
-                _beside(weights, torch.float32, (tokens, top_k), "weights", y),
-                None if residual is None else _beside(residual, torch.bfloat16, (tokens, n), "residual", y),
-                _beside(out, torch.bfloat16, (tokens, n), "out", y),
-                tokens,
-                top_k,
-                n,
-                _stream_ptr(stream),
-            )
-        )
+            out = y.new_empty((tokens, n))
+        _check(lib().bsr_moe_combine(y_ptr, r, pos_ptr, w_ptr, res_ptr, _ptr(out, bf16, (tokens, n), "out", index),
+                                     tokens, top_k, n, _raw_stream(stream, index)))
     return out
 
 
 def w4g_moe_mlp_scratch_bytes(tokens: int, experts: int, top_k: int, inner: int, k: int) -> int:
-    return int(lib().bsr_w4g_moe_mlp_scratch_bytes(tokens, experts, top_k, inner, k))
+    return lib().bsr_w4g_moe_mlp_scratch_bytes(tokens, experts, top_k, inner, k)
 
 
 def w4g_moe_mlp(x, logits, gate, up, down, top_k: int, renormalize: bool = True, residual=None, out=None,
@@ -1026,31 +1012,24 @@ def w4g_moe_mlp(x, logits, gate, up, down, top_k: int, renormalize: bool = True,
     with [E, K, inner/2].  The same results as :func:`moe_route`,
     :func:`w4g_proj_grouped`, :func:`silu_mul` and :func:`moe_combine` called
     one after the other."""
-    torch = _torch()
-    with _on(x):
-        tokens, k = _dims(x, 2, "x")
-        experts = _dims(logits, 2, "logits")[1]
-        inner = _dims(gate[0], 3, "gate codes")[1]
+    bf16 = _torch().bfloat16
+    index, here = _like(x, "x")
+    tokens, k = _dims(x, 2, "x")
+    experts = _dims(logits, 2, "logits")[1]
+    inner = _dims(gate[0], 3, "gate codes")[1]
+    x_ptr = _ptr(x, bf16, (tokens, k), "x", index)
+    kind = _logits_type(logits)
+    l_ptr = _ptr(logits, logits.dtype, (tokens, experts), "logits", index)
+    gate = _w4g_weight(*gate, (experts,), inner, k, index, "gate")
+    up = _w4g_weight(*up, (experts,), inner, k, index, "up")
+    down = _w4g_weight(*down, (experts,), k, inner, index, "down")
+    res_ptr = None if residual is None else _ptr(residual, bf16, (tokens, k), "residual", index)
+    with here:
         if out is None:
-            out = _empty((tokens, k), torch.bfloat16, x)
-        _check(
-            lib().bsr_w4g_moe_mlp(
-                _dev(x, torch.bfloat16, (tokens, k), "x"),
-                _beside(logits, logits.dtype, (tokens, experts), "logits", x),
-                _logits_type(logits),
-                _w4g_weight(*gate, (experts,), inner, k, x, "gate"),
-                _w4g_weight(*up, (experts,), inner, k, x, "up"),
-                _w4g_weight(*down, (experts,), k, inner, x, "down"),
-                None if residual is None else _beside(residual, torch.bfloat16, (tokens, k), "residual", x),
-                _beside(out, torch.bfloat16, (tokens, k), "out", x),
-                tokens,
-                experts,
-                int(top_k),
-                1 if renormalize else 0,
-                inner,
-                k,
-                *_scratch(scratch, w4g_moe_mlp_scratch_bytes(tokens, experts, top_k, inner, k), x),
-                _stream_ptr(stream),
-            )
-        )
+            out = x.new_empty((tokens, k))
+        need = lib().bsr_w4g_moe_mlp_scratch_bytes(tokens, experts, top_k, inner, k)
+        _check(lib().bsr_w4g_moe_mlp(x_ptr, l_ptr, kind, gate, up, down, res_ptr,
+                                     _ptr(out, bf16, (tokens, k), "out", index), tokens, experts, int(top_k),
+                                     1 if renormalize else 0, inner, k, *_scratch(scratch, need, x),
+                                     _raw_stream(stream, index)))
     return out

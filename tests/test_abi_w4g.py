@@ -125,11 +125,15 @@ def test_binding_refuses_before_the_library():
     with pytest.raises(ValueError, match="CUDA"):
         bsr.w4g_proj(a, q, s)
     with pytest.raises(ValueError, match="dimensions"):
-        bsr.w4g_proj(a[0], q, s)
-    with pytest.raises(ValueError, match="dimensions"):
+        bsr._dims(a[0], 2, "a")
+    with pytest.raises(ValueError, match="CUDA"):
         bsr.w4g_proj_grouped(a, torch.zeros(2, dtype=torch.int32), q, s)
     with pytest.raises(TypeError):
         bsr.w4g_proj([1.0], q, s)
+    for bad, error in ((a.half(), TypeError), (a.t(), ValueError), (a[:1], ValueError), (a, ValueError),
+                       (None, TypeError)):
+        with pytest.raises(error):
+            bsr._ptr(bad, torch.bfloat16, (2, 64), "a", 0)
     with pytest.raises(ValueError, match="top_k"):
         bsr.moe_route(torch.zeros(2, 4), 5)
     with pytest.raises(TypeError, match="float32 or bfloat16"):
@@ -137,4 +141,4 @@ def test_binding_refuses_before_the_library():
     for groups, kind, error in ((3, torch.bfloat16, ValueError), (1, torch.float32, TypeError),
                                 (4, torch.bfloat16, ValueError), (0, torch.bfloat16, ValueError)):
         with pytest.raises(error):
-            bsr._w4g_weight(q, torch.zeros(8, groups, dtype=kind), None, (), 8, 64, a, "w")
+            bsr._w4g_weight(q, torch.zeros(8, groups, dtype=kind), None, (), 8, 64, -1, "w")
