@@ -9,9 +9,10 @@
 // positions come from counts, not from atomically drawn tickets (the only
 // atomics are integer histogram counts).
 //
-// One warp per token; lane l holds experts l, l + 32, ...: a logit as an
-// unsigned key of the same order (0 = masked).  Each slot takes one hardware
-// warp maximum over keys and one warp minimum over the indices that hold it.
+// One warp per token (up to four in turn, for their latencies); lane l holds
+// experts l, l + 32, ...: a logit as an unsigned key of the same order (0 =
+// masked).  Each slot takes one hardware warp maximum over keys and one warp
+// minimum over the indices that hold it.
 // A block of tokens counts its pairs by expert.  With one block the same
 // launch groups them; otherwise a second launch (programmatic dependent, same
 // blocks) sums the counts of the blocks before it and the totals, then places
@@ -31,10 +32,12 @@
 namespace bsr {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kHeld = 4;  // rounds of 32 pairs whose ids a warp keeps in registers
 constexpr int kMaxBlocks = 128;
-constexpr int kMinBlockTokens = 128;
+constexpr int kMinBlockTokens = 32;   // a token per warp
+constexpr int kOneBlockTokens = 64;   // at most this many in a single block: one launch, 7 us where two take 9
 
 // Order-preserving key of a logit; 0 marks a masked expert.  +0 and -0 share
 // a key.
@@ -64,70 +67,109 @@ struct RouteArgs {
   int32_t* counts;  // [blocks, experts]
 };
 
-// The chosen experts of one token: slot j's id and weight end in lane j.
-template <int V>
-__device__ __forceinline__ void route_token(const RouteArgs& r, long long t, int lane, int* hist) {
-  uint32_t key[V];
-  float top = 0.0f, all = 0.0f;
-  const size_t row = (size_t)t * (size_t)r.experts;
+// The chosen experts of TP tokens t, t + step, ..., one step of each in turn so
+// that the warp reductions' latencies overlap: slot j's id and weight end in
+// lane j.  Each lane keeps its largest key and that key's expert; only the
+// lane whose expert was chosen looks through its keys again.
+template <int V, int TP>
+__device__ __forceinline__ void route_tokens(const RouteArgs& r, long long t, long long step, long long t1, int lane,
+                                             int* hist) {
+  uint32_t key[TP][V], best[TP], my_key[TP];
+  unsigned best_at[TP];
+  int my_id[TP];
+  float top[TP], all[TP];
+  bool left[TP];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * 32 + lane;
-    float x = -INFINITY;
-    if (e < r.experts)
-      x = r.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(r.logits)[row + e] << 16)
-                 : static_cast<const float*>(r.logits)[row + e];
-    key[v] = logit_key(x);
+  for (int p = 0; p < TP; ++p) {
+    const long long tp = t + p * step;
+    left[p] = tp < t1;
+    const size_t row = (size_t)(left[p] ? tp : t) * (size_t)r.experts;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = v * 32 + lane;
+      float x = -INFINITY;
+      if (left[p] && e < r.experts)
+        x = r.bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(r.logits) + row + e) << 16)
+                   : __ldg(static_cast<const float*>(r.logits) + row + e);
+      key[p][v] = logit_key(x);
+    }
   }
-  int my_id = -1;
-  uint32_t my_key = 0u;
+  auto rescan = [&](int p) {
+    best[p] = key[p][V - 1];
+    best_at[p] = (unsigned)((V - 1) * 32 + lane);
+#pragma unroll
+    for (int v = V - 2; v >= 0; --v)
+      if (key[p][v] >= best[p]) {
+        best[p] = key[p][v];
+        best_at[p] = (unsigned)(v * 32 + lane);
+      }
+  };
+#pragma unroll
+  for (int p = 0; p < TP; ++p) {
+    rescan(p);
+    my_id[p] = -1;
+    my_key[p] = 0u;
+    top[p] = all[p] = 0.0f;
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best[p]);
+    if (m) top[p] = key_logit(m);
+    if (!r.renorm && m) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (key[p][v]) all[p] += shifted_exp(key_logit(key[p][v]), top[p]);
+    }
+  }
   for (int j = 0; j < r.top_k; ++j) {
-    uint32_t best = 0u;
+    uint32_t m[TP];
+    unsigned at[TP];
 #pragma unroll
-    for (int v = 0; v < V; ++v) best = max(best, key[v]);
-    best = __reduce_max_sync(0xFFFFFFFFu, best);
-    if (best == 0u) break;  // every expert left is masked
-    unsigned at = UINT_MAX;
+    for (int p = 0; p < TP; ++p) m[p] = __reduce_max_sync(0xFFFFFFFFu, best[p]);
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] == best) at = (unsigned)(v * 32 + lane);
-    at = __reduce_min_sync(0xFFFFFFFFu, at);
-    if (j == 0) {
-      top = key_logit(best);
-      if (!r.renorm) {
+    for (int p = 0; p < TP; ++p) at[p] = __reduce_min_sync(0xFFFFFFFFu, best[p] == m[p] ? best_at[p] : UINT_MAX);
+#pragma unroll
+    for (int p = 0; p < TP; ++p) {
+      if (m[p] == 0u) continue;  // every expert left is masked
+      if (lane == j) {
+        my_id[p] = (int)at[p];
+        my_key[p] = m[p];
+      }
+      if ((at[p] & 31u) == (unsigned)lane) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if (key[v]) all += shifted_exp(key_logit(key[v]), top);
+          if ((unsigned)(v * 32 + lane) == at[p]) key[p][v] = 0u;
+        rescan(p);
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if ((unsigned)(v * 32 + lane) == at) key[v] = 0u;
-    if (lane == j) {
-      my_id = (int)at;
-      my_key = best;
-    }
   }
-  const float p = my_id >= 0 ? shifted_exp(key_logit(my_key), top) : 0.0f;
-  float total = r.renorm ? p : all;
 #pragma unroll
-  for (int off = 16; off; off >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, off);
-  if (lane < r.top_k) {
-    const size_t at = (size_t)t * r.top_k + lane;
-    r.ids[at] = my_id;
-    r.weights[at] = my_id >= 0 ? p / total : 0.0f;
-    if (my_id >= 0) atomicAdd(&hist[my_id], 1);
+  for (int p = 0; p < TP; ++p) {
+    const float e = my_id[p] >= 0 ? shifted_exp(key_logit(my_key[p]), top[p]) : 0.0f;
+    float total = r.renorm ? e : all[p];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, off);
+    if (lane < r.top_k && left[p]) {
+      const size_t at = (size_t)(t + p * step) * r.top_k + lane;
+      r.ids[at] = my_id[p];
+      r.weights[at] = my_id[p] >= 0 ? e / total : 0.0f;
+      if (my_id[p] >= 0) atomicAdd(&hist[my_id[p]], 1);
+    }
   }
 }
 
 template <int V>
 __device__ void route_block(const RouteArgs& r, int* hist) {
+  constexpr int TP = V <= 4 ? 4 : V <= 8 ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < r.experts; e += kThreads) hist[e] = 0;
   __syncthreads();
   const long long t0 = blockIdx.x * r.block_tokens;
   const long long t1 = min(r.tokens, t0 + r.block_tokens);
-  for (long long t = t0 + warp; t < t1; t += kWarps) route_token<V>(r, t, lane, hist);
+  if (TP == 1 || t1 - t0 <= kWarps) {
+    for (long long t = t0 + warp; t < t1; t += kWarps) route_tokens<V, 1>(r, t, kWarps, t1, lane, hist);
+  } else if (TP == 2 || t1 - t0 <= 2 * kWarps) {
+    for (long long t = t0 + warp; t < t1; t += 2 * kWarps) route_tokens<V, 2>(r, t, kWarps, t1, lane, hist);
+  } else {
+    for (long long t = t0 + warp; t < t1; t += TP * kWarps) route_tokens<V, TP>(r, t, kWarps, t1, lane, hist);
+  }
   __syncthreads();
 }
 
@@ -153,47 +195,70 @@ __device__ void scan_experts(const int* total, int* first, int experts) {
   __syncthreads();
 }
 
-// Places the block's pairs.  start[e]: position of the block's first pair of
-// expert e.  warp_counts [kWarps][experts].
-__device__ void place_pairs(const RouteArgs& r, const int* start, int* warp_counts) {
+// A warp's contiguous part of the block's pairs, the ids of its first rounds
+// in registers.
+struct Part {
+  long long a, b;
+  int id[kHeld];
+};
+__device__ __forceinline__ Part load_part(const RouteArgs& r) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long p0 = blockIdx.x * r.block_tokens * r.top_k;
   const long long p1 = min(r.tokens * r.top_k, p0 + r.block_tokens * r.top_k);
   long long part = (p1 - p0 + kWarps - 1) / kWarps;
   part = (part + 31) / 32 * 32;
-  const long long a = min(p1, p0 + warp * part), b = min(p1, a + part);
+  Part w;
+  w.a = min(p1, p0 + warp * part);
+  w.b = min(p1, w.a + part);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const long long p = w.a + i * 32 + lane;
+    w.id[i] = p < w.b ? r.ids[p] : -1;
+  }
+  return w;
+}
+
+// Places the block's pairs.  start[e]: position of the block's first pair of
+// expert e.  warp_counts [kWarps][experts].
+__device__ void place_pairs(const RouteArgs& r, const Part& w, const int* start, int* warp_counts) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* mine = warp_counts + warp * r.experts;
-  for (int i = threadIdx.x; i < kWarps * r.experts; i += kThreads) warp_counts[i] = 0;
-  __syncthreads();
-  for (long long p = a + lane; p < b; p += 32) {
+  for (int e = lane; e < r.experts; e += 32) mine[e] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (w.id[i] >= 0) atomicAdd(&mine[w.id[i]], 1);
+  for (long long p = w.a + kHeld * 32 + lane; p < w.b; p += 32) {
     const int id = r.ids[p];
     if (id >= 0) atomicAdd(&mine[id], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < r.experts; e += kThreads) {
     int at = start[e];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int c = warp_counts[w * r.experts + e];
-      warp_counts[w * r.experts + e] = at;
+#pragma unroll 8
+    for (int i = 0; i < kWarps; ++i) {
+      const int c = warp_counts[i * r.experts + e];
+      warp_counts[i * r.experts + e] = at;
       at += c;
     }
   }
   __syncthreads();
-  for (long long p = a; p < b; p += 32) {
-    const bool in = p + lane < b;
-    const int id = in ? r.ids[p + lane] : -1;
+  auto round = [&](long long p, int id) {  // p: this lane's pair
     const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
     int at = -1;
     if (id >= 0) {
       at = mine[id] + __popc(same & ((1u << lane) - 1u));
-      r.rows[at] = (int)((p + lane) / r.top_k);
+      r.rows[at] = (int)(p / r.top_k);
     }
-    if (in) r.pos[p + lane] = at;
+    if (p < w.b) r.pos[p] = at;
     __syncwarp();
     if (id >= 0 && (same >> lane) == 1u) mine[id] = at + 1;  // the last lane of each set
     __syncwarp();
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (w.a + i * 32 < w.b) round(w.a + i * 32 + lane, w.id[i]);
+  for (long long p = w.a + kHeld * 32; p < w.b; p += 32) round(p + lane, p + lane < w.b ? r.ids[p + lane] : -1);
 }
 
 // rows[] past the last group, the block's share of them
@@ -215,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs r) {
     int* first = hist + r.experts;
     scan_experts(hist, first, r.experts);
     for (int e = threadIdx.x; e <= r.experts; e += kThreads) r.offsets[e] = first[e];
-    place_pairs(r, first, first + r.experts + 1);
+    place_pairs(r, load_part(r), first, first + r.experts + 1);
     fill_tail(r, first[r.experts]);
   } else {
     for (int e = threadIdx.x; e < r.experts; e += kThreads)
@@ -233,6 +298,7 @@ __global__ void __launch_bounds__(kThreads) route_group_kernel(const RouteArgs r
   for (int e = threadIdx.x; e < r.experts; e += kThreads) before[e] = 0;
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Part w = load_part(r);  // on its way while the counts are summed
   // counts of all blocks, and of the blocks before this one
   const int lanes_e = r.experts < kThreads ? r.experts : kThreads;
   const int parts = kThreads / lanes_e;
@@ -258,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) route_group_kernel(const RouteArgs r
   __syncthreads();
   for (int e = threadIdx.x; e < r.experts; e += kThreads) total[e] = first[e] + before[e];
   __syncthreads();
-  place_pairs(r, total, warp_counts);
+  place_pairs(r, w, total, warp_counts);
   fill_tail(r, used);
 }
 
@@ -385,6 +451,7 @@ cudaError_t launch_combine_v(const uint16_t* y, long long y_rows, const int32_t*
 }  // namespace
 
 long long route_block_tokens(long long tokens) {
+  if (tokens <= kOneBlockTokens) return kOneBlockTokens;
   const long long b = (tokens + kMaxBlocks - 1) / kMaxBlocks;
   return b < kMinBlockTokens ? kMinBlockTokens : b;
 }

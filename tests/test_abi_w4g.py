@@ -84,9 +84,9 @@ def test_route(L):
     for i in range(5):
         assert call(out=tuple(None if j == i else A for j in range(5))) == EINVAL
         assert call(out=tuple(P(258) if j == i else A for j in range(5))) == EALIGN
-    assert L.bsr_moe_route_scratch_bytes(128, 8) == 0
+    assert L.bsr_moe_route_scratch_bytes(64, 8) == 0
     need = L.bsr_moe_route_scratch_bytes(129, 8)
-    assert need == 2 * 8 * 4 and L.bsr_moe_route_scratch_bytes(10 ** 6, 64) <= 128 * 64 * 4
+    assert need == 5 * 8 * 4 and L.bsr_moe_route_scratch_bytes(10 ** 6, 64) <= 128 * 64 * 4
     assert call(t=129) == ESCRATCH and call(t=129, scratch=A, nbytes=need - 1) == ESCRATCH
     assert call(t=129, scratch=P(258), nbytes=need) == EALIGN
 
