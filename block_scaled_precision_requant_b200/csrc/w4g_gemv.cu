@@ -30,6 +30,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
+#ifdef W4G_FORCE
+#include <cstdlib>
+#endif
 #include <mutex>
 
 #include "common.cuh"
@@ -255,22 +259,30 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   const int r8 = ((g8 & 1) << 2) | (g8 & 2) | (g8 >> 2);  // bit reversal
   const int groups = g.k / G;
 
-  // The activation rows of an item: row tt * 8 + g8 in this lane.
-  struct Rows {
-    const uint16_t* p[NT];
+  // The activation rows of an item: row tt * 8 + g8 in this lane; -1 for none.
+  // The index is read an item ahead, and looked at only when its item begins.
+  struct Index {
+    int r[NT];
   };
-  auto rows_of = [&](const Item& t) {
-    Rows x;
+  auto index_of = [&](const Item& t) {
+    Index x;
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) {
       const int r = tt * 8 + g8;
-      x.p[tt] = nullptr;
-      if (r < t.cnt) {
-        const long long src = g.rows ? (long long)g.rows[t.row0 + r] : (long long)t.row0 + r;
-        if (src >= 0 && src < g.a_rows) x.p[tt] = g.a + (size_t)src * (size_t)g.k + t4 * (G / 4);
-      }
+      x.r[tt] = -1;
+      if (r < t.cnt) x.r[tt] = g.rows ? __ldg(g.rows + t.row0 + r) : t.row0 + r;
     }
     return x;
+  };
+  struct Rows {
+    const uint16_t* p[NT];
+  };
+  auto rows_of = [&](const Index& x) {
+    Rows q;
+#pragma unroll
+    for (int tt = 0; tt < NT; ++tt)
+      q.p[tt] = x.r[tt] >= 0 && x.r[tt] < g.a_rows ? g.a + (size_t)x.r[tt] * (size_t)g.k + t4 * (G / 4) : nullptr;
+    return q;
   };
   // One segment's activations: of each group, this lane's G/4 elements.
   struct Acts {
@@ -342,22 +354,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 
   bool dead = false;
   Item next = {};
-  Rows next_rows = {};
+  Index next_index = {};
   Meta meta = {};
   if (first < items) {
     next = find(first);
-    next_rows = rows_of(next);
+    next_index = index_of(next);
     meta = load_meta(next, wk * GS * NT, 0);
   }
   int slot = 0;
   uint32_t phase = 0;
   for (int it = first; it < items; it += step) {
     const Item t = next;
-    const Rows rows = next_rows;
+    const Rows rows = rows_of(next_index);
     const int n0 = t.blk * rb;
     if (it + step < items) {
       next = find(it + step);
-      next_rows = rows_of(next);
+      next_index = index_of(next);
     }
     float tot[RT][NT][4];
 #pragma unroll
@@ -547,30 +559,43 @@ cudaError_t launch_g(const CUtensorMap& tm, const W4gArgs& g, const W4gGemvPlan&
 W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   W4gGemvPlan p = {};
   p.chunks = (g.k + kChunk - 1) / kChunk;
+  // at least two chunks per warp: an item's fixed cost (its lookup, the first
+  // activations, the sum over warps) is that of two tiles' chunks.  By K only,
+  // so that the order of a row's sum is.
   p.ks = 1;
-  while (p.ks < kWarps && p.ks * 2 <= p.chunks) p.ks *= 2;
+  while (p.ks < kWarps && p.ks * 4 <= p.chunks) p.ks *= 2;
   const int ngrp = kWarps / p.ks;
-  // activation rows per item by the rows that an expert gets on average
-  const long long active = g.rows_max < g.experts ? g.rows_max : g.experts;
-  p.nt = (g.rows_max + active - 1) / active <= 8 ? 1 : 2;
-  const long long tok = 8 * p.nt;
-  const long long tiles = active + (g.rows_max - active) / tok;
+  const int per_warp = (p.chunks + p.ks - 1) / p.ks;
+  // experts with rows, for choices without preference, and their items' rows
+  const double pairs = (double)g.rows_max, experts = (double)g.experts;
+  double active = g.experts == 1 ? 1.0 : experts * (1.0 - pow(1.0 - 1.0 / experts, pairs));
+  const double mean = pairs / active;
+  p.nt = mean <= 8.0 ? 1 : 2;
+  const int tok = 8 * p.nt;
+  const double tiles = g.experts == 1 ? (double)((g.rows_max + tok - 1) / tok)
+                                      : active * (mean <= 0.5 * tok ? 1.0 : 0.5 + mean / tok);
   // rt tiles of tr rows per item: the least estimated time over whole waves
-  // of two CTAs per SM
-  const long long slots_all = 2LL * num_sms * ngrp;
+  // of two CTAs per SM.  Measured per wave: 2.3 us + 1.25 us per tile and
+  // chunk of a warp (64 rows, K = 2048: 7.6 us; 16 rows: 3.5 us); tiles below
+  // 13 rows stream less but take as long.
+  const double slots_all = 2.0 * num_sms * ngrp;
   double best = 0.0;
   for (int rt = 4; rt >= 1; --rt)
     for (int tr = 16; tr >= 8; --tr) {
-      const int rb = rt * tr;
-      const long long items = ((g.n + rb - 1) / rb) * tiles;
-      const long long waves = (items + slots_all - 1) / slots_all;
-      const double cost = (double)waves * ((rb > 13 * rt ? rb : 13 * rt) + 8);
+      const double items = (double)((g.n + rt * tr - 1) / (rt * tr)) * tiles;
+      const double cost = ceil(items / slots_all) * (2.3 + per_warp * rt * 1.25 * (tr > 13 ? tr : 13) / 16.0);
       if (best == 0.0 || cost < best - 1e-9) {
         best = cost;
         p.rt = rt;
         p.tr = tr;
       }
     }
+#ifdef W4G_FORCE
+  if (getenv("W4G_RB")) {
+    p.rt = atoi(getenv("W4G_RB")) / 100;
+    p.tr = atoi(getenv("W4G_RB")) % 100;
+  }
+#endif
   const int rb = p.rt * p.tr;
   p.nblk = (g.n + rb - 1) / rb;
   // slots: as many as leave room for two CTAs per SM (228 KB less 1 KB per
@@ -579,7 +604,8 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   p.slots = 6;
   while (p.slots > p.rt + 1 && gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total > 115712u) --p.slots;
   p.smem = gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total;
-  const long long items = (long long)p.nblk * (tiles + active);  // ragged tails add at most one tile per expert
+  // of any grouping: each expert's last tile may be ragged
+  const long long items = (long long)p.nblk * ((g.rows_max < g.experts ? g.rows_max : g.experts) + g.rows_max / tok);
   const long long ctas = (items + ngrp - 1) / ngrp;
   p.grid = (int)(ctas < 2LL * num_sms ? ctas : 2LL * num_sms);
   return p;
