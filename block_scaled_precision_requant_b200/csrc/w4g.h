@@ -39,7 +39,7 @@ cudaError_t launch_w4g_gemv(const CUtensorMap& tm_q, const W4gArgs& g, const W4g
 
 // Many rows per expert: the tcgen05 tensor cores, tiles of 128 weight rows x
 // bm activation rows.  Tensor maps: codes [experts * N, K/2] bytes, box 128
-// rows x 32 bytes, 32-byte swizzle; activations [a_rows, K] BF16, box bm rows
+// rows x 64 bytes, 64-byte swizzle; activations [a_rows, K] BF16, box bm rows
 // x 64, 128-byte swizzle.  Takes no row index.
 struct W4gGemmPlan {
   int bm, grid;

@@ -159,8 +159,8 @@ bsr_status plan_product(Product& p, const bsr::W4gArgs& g, const Device& d) {
                      CU_TENSOR_MAP_SWIZZLE_128B, "w4g codes");
   }
   p.gemm = bsr::w4g_gemm_plan(g, d.num_sms);
-  const bsr_status st = encode_2d(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, wpitch, wrows, wpitch, 32, 128,
-                                  CU_TENSOR_MAP_SWIZZLE_32B, "w4g codes");
+  const bsr_status st = encode_2d(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, wpitch, wrows, wpitch, 64, 128,
+                                  CU_TENSOR_MAP_SWIZZLE_64B, "w4g codes");
   if (st != BSR_OK) return st;
   return encode_2d(&p.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.a, (uint64_t)g.k, (uint64_t)g.a_rows, (uint64_t)g.k * 2,
                    64, (uint32_t)p.gemm.bm, CU_TENSOR_MAP_SWIZZLE_128B, "w4g activations");

@@ -7,10 +7,10 @@
 //
 // Tile: 128 weight rows (tensor-memory lanes, MMA M) x BM activation rows of
 // one expert (columns, MMA N).  The codes are the A operand and go through
-// tensor memory: a stage's codes (128 rows x 64 elements, 4 KB) come by TMA,
+// tensor memory: a stage's codes (128 rows x 128 elements, 8 KB) come by TMA,
 // two sets of four warps unpack alternate stages to BF16 pairs (10
 // instructions per 8 elements) and store them with tcgen05.st as the A operand of `tcgen05.mma kind::f16`.
-// Through shared memory the unpacked tile (16 KB per stage, written once and
+// Through shared memory the unpacked tile (32 KB per stage, written once and
 // read once) would compete with the activation tile for its bandwidth.
 // Activations (B operand) come by TMA into 128-byte-swizzled tiles, so a row
 // index is resolved by a copy of the rows beforehand (w4g_gather_kernel): the
@@ -45,24 +45,28 @@ namespace bsr {
 namespace {
 
 constexpr int kBn = 128;       // weight rows per tile
-constexpr int kKs = 64;        // elements of K per stage
+constexpr int kKs = 128;       // elements of K per stage
 constexpr int kRaw = kBn * kKs / 2;
 constexpr int kThreads = 640;
 constexpr int kDeqWarp0 = 4, kEpiWarp0 = 12;
 constexpr int kDeqWarps = 8, kEpiWarps = 8;
-constexpr int kAStages = 4;    // unpacked stages in tensor memory, 32 columns each
-constexpr uint32_t kColA = 384, kTmemCols = 512;
+constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 12;
 constexpr size_t kSmemMax = 232448;
 constexpr int kLaunchRegs = 96, kCtrlRegs = 48;
 
 template <int BM>
 struct Cfg {
-  static constexpr int TBUF = 384 / BM < 6 ? 384 / BM : 6;
+  // tensor memory: the groups' accumulators, then the unpacked stages of 64
+  // columns (128 elements of K, two per column)
+  static constexpr int ASTAGES = BM == 192 ? 2 : 4;
+  static constexpr uint32_t COL_A = kTmemCols - 64u * ASTAGES;
+  static constexpr int TBUF = (int)COL_A / BM < 6 ? (int)COL_A / BM : 6;
   static constexpr int COLS = BM / 2;                     // columns per epilogue warp
   static constexpr int CH = BM == 192 ? 2 : 1;            // chunks that go through registers at once
   static constexpr int CW = COLS / CH;                    // columns of a chunk: 48, 64, 32, 16
-  static constexpr int STAGE = kRaw + BM * 128;
+  static constexpr int ACT = BM * 256;                    // two 128-byte-swizzled tiles of 64 elements of K
+  static constexpr int STAGE = kRaw + ACT;
   // register split: launched with kLaunchRegs per thread
   static constexpr int EPI_REGS = BM == 192 ? 168 : 136;
   static constexpr int DEQ_REGS = BM == 192 ? 48 : 80;
@@ -71,7 +75,7 @@ struct Cfg {
 
 struct Ctrl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t aready[kAStages];
+  uint64_t aready[4];
   uint64_t tfull[6], tempty[6];
   uint64_t drain;
   uint32_t tmem_base;
@@ -216,9 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&ctrl->full[s], 1);
-      mbar_init(&ctrl->empty[s], 1 + kDeqWarps / 2);  // the MMA commit + the stage's unpacking warps
+      mbar_init(&ctrl->empty[s], 1 + kDeqWarps);  // the MMA commit + the unpacking warps
     }
-    for (int s = 0; s < kAStages; ++s) mbar_init(&ctrl->aready[s], kDeqWarps / 2);
+    for (int s = 0; s < C::ASTAGES; ++s) mbar_init(&ctrl->aready[s], kDeqWarps);
     for (int b = 0; b < C::TBUF; ++b) {
       mbar_init(&ctrl->tfull[b], 1);
       mbar_init(&ctrl->tempty[b], kEpiWarps);
@@ -311,8 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             uint8_t* st = stage_ptr(p.i);
             mbar_arrive_expect_tx(&ctrl->full[p.i], C::STAGE);
-            tma_load_2d(st + BM * 128, &tm_q, &ctrl->full[p.i], ks * (kKs / 2), t.e * g.n + t.n0);
+            tma_load_2d(st + C::ACT, &tm_q, &ctrl->full[p.i], ks * (kKs / 2), t.e * g.n + t.n0);
             tma_load_2d(st, &tm_a, &ctrl->full[p.i], ks * kKs, t.row0);
+            tma_load_2d(st + BM * 128, &tm_a, &ctrl->full[p.i], ks * kKs + 64, t.row0);  // zeros past K
           }
           __syncwarp();
           ++it;
@@ -334,22 +339,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       constexpr uint32_t idesc = idesc_bf16(kBn, BM);
       const uint64_t b_desc0 = smem_desc_k_sw128(smem_u32(smem));
-      // MMAs [j0, j1) of a stage (16 elements of K each) into the current
-      // buffer, onto what it holds if `acc`; then, if asked, the buffer's and
-      // the stage's commits
-      auto mmas = [&](int j0, int j1, uint32_t acc, bool buffer, bool stage) {
+      // The MMAs of the stage's group `gi` (16 elements of K each) into the
+      // current buffer and its commit; after the last group the stage's
+      auto group = [&](int gi, bool last) {
         const uint64_t b = b_desc0 + (uint64_t)(p.i * (C::STAGE >> 4));
-        const uint32_t a = tmem + kColA + (uint32_t)ap.i * 32u;
+        const uint32_t a = tmem + C::COL_A + (uint32_t)ap.i * 64u;
         const uint32_t d = tmem + (uint32_t)(tp.i * BM);
         if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j >= j0 && j < j1) mma_ts(d, a + (uint32_t)j * 8u, b + (uint64_t)(j * 2), idesc, j > j0 ? 1u : acc);
-          if (buffer) tc_commit(&ctrl->tfull[tp.i]);
-          if (stage) tc_commit(&ctrl->empty[p.i]);
+          for (int j = 0; j < G / 16; ++j) {
+            const int k16 = gi * (G / 16) + j;  // of the stage's 8: tile k16 / 4, 32 bytes each
+            mma_ts(d, a + (uint32_t)k16 * 8u, b + (uint64_t)((k16 >> 2) * (BM * 128 >> 4) + (k16 & 3) * 2), idesc,
+                   j > 0 ? 1u : 0u);
+          }
+          tc_commit(&ctrl->tfull[tp.i]);
+          if (last) tc_commit(&ctrl->empty[p.i]);
         }
         __syncwarp();
-        if (buffer) tp.next(C::TBUF);
+        tp.next(C::TBUF);
       };
       auto buffer_wait = [&]() {
         const bool in = mbar_wait(&ctrl->tempty[tp.i], tp.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_MMA);
@@ -357,26 +364,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
         for (int ks = 0; ks < kstages; ++ks) {
-          if ((G != 128 || (ks & 1) == 0) && !(ok = buffer_wait())) break;
+          const int count = min(kKs, g.k - ks * kKs) / G;  // groups of the stage
+          if (!(ok = buffer_wait())) break;
           ok = mbar_wait(&ctrl->aready[ap.i], ap.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA);
           ok = !__any_sync(0xFFFFFFFFu, !ok);
           if (!ok) break;
           tc_fence_after();
-          if constexpr (G == 32) {
-            const bool two = ks * kKs + 32 < g.k;
-            mmas(0, 2, 0u, true, !two);
-            if (two) {
+#pragma unroll
+          for (int gi = 0; gi < kKs / G; ++gi) {
+            if (gi >= count) break;
+            if (gi > 0) {
               if (!(ok = buffer_wait())) break;
               tc_fence_after();
-              mmas(2, 4, 0u, true, true);
             }
-          } else if constexpr (G == 64) {
-            mmas(0, 4, 0u, true, true);
-          } else {
-            mmas(0, 4, (uint32_t)(ks & 1), (ks & 1) != 0, true);
+            group(gi, gi + 1 == count);
           }
+          if (!ok) break;
           p.next(stages);
-          ap.next(kAStages);
+          ap.next(C::ASTAGES);
         }
       }
       // every MMA issued so far has completed once this commit arrives
@@ -387,14 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kEpiWarp0) {
     setmaxnreg_dec<C::DEQ_REGS>();
     // ------------------------------------------------------------------ unpack
-    // two sets of four warps take alternate stages
-    const int q = warp & 3, set = (warp - kDeqWarp0) >> 2;
+    // warp w: lanes 32 (w % 4).., K half (w - 4) / 4 of each stage
+    const int q = warp & 3, half = (warp - kDeqWarp0) >> 2;
     const int row = q * 32 + lane;
-    // the row's 32 bytes: 16-byte halves exchanged by the 32-byte swizzle
-    const uint32_t roff = (uint32_t)(BM * 128 + row * 32), rsw = (uint32_t)((row >> 2) & 1) * 16u;
-    const uint32_t t_addr = tmem + ((uint32_t)(q * 32) << 16) + kColA;
+    // the row's 64 bytes, this half's 32: 16-byte quarters under the 64-byte
+    // swizzle
+    const uint32_t roff = (uint32_t)(C::ACT + row * 64), rsw = (uint32_t)((row >> 1) & 3) * 16u;
+    const uint32_t t_addr = tmem + ((uint32_t)(q * 32) << 16) + C::COL_A + (uint32_t)half * 32u;
     Pos p, ap, fp;  // stage, operand buffer, the stage whose MMAs free that buffer
-    // The set's last stage whose stores are in flight: they are waited for, and
+    // The last stage whose stores are in flight: they are waited for, and
     // the stage handed on, once the next stage's codes have been read, so that
     // the stores' latency passes during the reads.
     int last_stage = -1, last_buf = 0;
@@ -417,82 +423,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileAt t = find(tile);
         if (t.n0 + row < g.n) zrow = g.zero + ((size_t)t.e * g.n + t.n0 + row) * (size_t)groups;
       }
-      // zero points of a stage's halves, as stored
+      // zero points of the half's two 32-element parts, as stored
       struct Zeros {
         uint8_t a, b;
       };
       auto zero_at = [&](int ks) {
-        const int g0 = ks * kKs / G, g1 = (ks * kKs + 32) / G;
+        const int k0 = ks * kKs + half * 64;
+        const int g0 = k0 / G, g1 = (k0 + 32) / G;
         Zeros z = {8, 8};
         if (zrow && g0 < groups) z.a = __ldg(zrow + g0);
         if (G == 32 && zrow && g1 < groups) z.b = __ldg(zrow + g1);
         return z;
       };
-      // this set's first stage of the tile; zero points two of its stages ahead
-      const int ks0 = (int)((it ^ (uint32_t)set) & 1u);
-      Zeros z0 = {8, 8}, z1 = {8, 8};
+      // of this and the next two stages
+      Zeros z0 = {8, 8}, z1 = {8, 8}, z2 = {8, 8};
       if (g.zero) {
-        z0 = zero_at(ks0);
-        z1 = zero_at(ks0 + 2);
+        z0 = zero_at(0);
+        z1 = zero_at(1);
+        z2 = zero_at(2);
       }
       for (int ks = 0; ks < kstages; ++ks, ++it) {
-        if (((it ^ (uint32_t)set) & 1u) == 0) {
-          uint32_t zc[2] = {0xBE00BE00u, 0xBE00BE00u};  // -8 / 64
-          if (g.zero) {
-            zc[0] = zero_pair(z0.a);
-            zc[1] = G == 32 ? zero_pair(z0.b) : zc[0];
-            z0 = z1;
-            z1 = zero_at(ks + 4);
-          }
-          ok = mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP);
+        uint32_t zc[2] = {0xBE00BE00u, 0xBE00BE00u};  // -8 / 64
+        if (g.zero) {
+          zc[0] = zero_pair(z0.a);
+          zc[1] = G == 32 ? zero_pair(z0.b) : zc[0];
+          z0 = z1;
+          z1 = z2;
+          z2 = zero_at(ks + 3);
+        }
+        ok = mbar_wait(&ctrl->full[p.i], p.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP);
+        if (__any_sync(0xFFFFFFFFu, !ok)) {
+          ok = false;
+          break;
+        }
+        const uint32_t raw = smem_u32(stage_ptr(p.i)) + roff;
+        uint32_t w[2][4];
+#pragma unroll
+        for (int hk = 0; hk < 2; ++hk)
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[hk][0]), "=r"(w[hk][1]), "=r"(w[hk][2]), "=r"(w[hk][3])
+                       : "r"(raw + ((uint32_t)(half * 32 + hk * 16) ^ rsw))
+                       : "memory");
+        finish();
+        // the operand buffer is free once the MMAs of ASTAGES stages ago have
+        // completed, which their stage's release says (this warp's own arrival
+        // for that stage is long past, and the stage cannot be released again
+        // before this warp reaches it)
+        if (it >= (uint32_t)C::ASTAGES) {
+          ok = mbar_wait(&ctrl->empty[fp.i], fp.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP);
           if (__any_sync(0xFFFFFFFFu, !ok)) {
             ok = false;
             break;
           }
-          const uint32_t raw = smem_u32(stage_ptr(p.i)) + roff;
-          uint32_t w[2][4];
-#pragma unroll
-          for (int hk = 0; hk < 2; ++hk)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[hk][0]), "=r"(w[hk][1]), "=r"(w[hk][2]), "=r"(w[hk][3])
-                         : "r"(raw + ((uint32_t)(hk * 16) ^ rsw))
-                         : "memory");
-          finish();
-          // the operand buffer is free once the MMAs of kAStages stages ago
-          // have completed, which their stage's release says (this set's own
-          // arrival for that stage is long past, and the stage cannot be
-          // released again before this warp reaches it)
-          if (it >= (uint32_t)kAStages) {
-            ok = mbar_wait(&ctrl->empty[fp.i], fp.phase, abort_flag, status, DEV_ERR_TIMEOUT_PREP);
-            if (__any_sync(0xFFFFFFFFu, !ok)) {
-              ok = false;
-              break;
-            }
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int hk = 0; hk < 2; ++hk) {
-            uint32_t v[16];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // low and high nibbles of the four bytes; byte j of each makes a
-              // pair of halves (a sign byte of `lo` is zero): the low nibble in
-              // bits 0-3, the high one in bits 4-7.  Bits below 256 read as
-              // BF16 are that integer times 2^-133.
-              const uint32_t lo = w[hk][i] & 0x0F0F0F0Fu, hi = w[hk][i] & 0xF0F0F0F0u;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[i * 4 + j] = fma_bf16x2(prmt(lo, hi, 0x8080u | (uint32_t)(j | (4 + j) << 8)), 0x7D007F00u,
-                                          zc[hk]);
-            }
-            tmem_st_x16(t_addr + (uint32_t)(ap.i * 32 + hk * 16), v);
-          }
-          last_stage = p.i;
-          last_buf = ap.i;
+          fp.next(stages);
         }
+        tc_fence_after();
+#pragma unroll
+        for (int hk = 0; hk < 2; ++hk) {
+          uint32_t v[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // low and high nibbles of the four bytes; byte j of each makes a
+            // pair of halves (a sign byte of `lo` is zero): the low nibble in
+            // bits 0-3, the high one in bits 4-7.  Bits below 256 read as BF16
+            // are that integer times 2^-133.
+            const uint32_t lo = w[hk][i] & 0x0F0F0F0Fu, hi = w[hk][i] & 0xF0F0F0F0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[i * 4 + j] =
+                  fma_bf16x2(prmt(lo, hi, 0x8080u | (uint32_t)(j | (4 + j) << 8)), 0x7D007F00u, zc[hk]);
+          }
+          tmem_st_x16(t_addr + (uint32_t)(ap.i * 64 + hk * 16), v);
+        }
+        last_stage = p.i;
+        last_buf = ap.i;
         p.next(stages);
-        ap.next(kAStages);
-        if (it >= (uint32_t)kAStages) fp.next(stages);
+        ap.next(C::ASTAGES);
       }
     }
     finish();
@@ -621,7 +627,7 @@ size_t smem_bytes(int stages, int experts) {
 template <int BM>
 int stage_count(int experts) {
   int s = kMaxStages;
-  while (s > kAStages + 1 && smem_bytes<BM>(s, experts) > kSmemMax) --s;
+  while (s > Cfg<BM>::ASTAGES + 1 && smem_bytes<BM>(s, experts) > kSmemMax) --s;
   return s;
 }
 
