@@ -2,6 +2,7 @@
 // of the expert router and combine.
 #pragma once
 
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -25,6 +26,27 @@ struct W4gArgs {
   int half_scale;          // scales are FP16
 };
 
+// What the host knows of the groups: the experts that have rows and their mean
+// number of rows, for choices without preference.
+struct W4gSpread {
+  double active, mean;
+  bool one;  // a single expert: all rows are its
+  // Tiles of `rows` activation rows over all experts; a group's last tile is
+  // half empty on average.
+  double tiles(int rows) const {
+    if (one) return std::ceil(mean / rows);
+    return active * (mean <= 0.5 * rows ? 1.0 : 0.5 + mean / rows);
+  }
+};
+inline W4gSpread w4g_spread(const W4gArgs& g) {
+  W4gSpread s;
+  const double experts = (double)g.experts, pairs = (double)g.rows_max;
+  s.one = g.experts == 1;
+  s.active = s.one ? 1.0 : experts * (1.0 - std::pow(1.0 - 1.0 / experts, pairs));
+  s.mean = pairs / s.active;
+  return s;
+}
+
 // Few rows per expert: warp-level tensor instructions fed by a streamed weight.
 // Items of rt tiles of tr (<= 16) weight rows x 8 nt activation rows, ks warps
 // along K; the codes' tensor map has boxes of tr rows x 128 bytes with the
@@ -32,6 +54,7 @@ struct W4gArgs {
 struct W4gGemvPlan {
   int tr, rt, nt, ks, slots, nblk, chunks, grid;
   size_t smem;
+  double us;  // estimated time
 };
 W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms);
 cudaError_t launch_w4g_gemv(const CUtensorMap& tm_q, const W4gArgs& g, const W4gGemvPlan& p, int* status,
@@ -43,6 +66,7 @@ cudaError_t launch_w4g_gemv(const CUtensorMap& tm_q, const W4gArgs& g, const W4g
 // x 64, 128-byte swizzle.  Takes no row index.
 struct W4gGemmPlan {
   int bm, grid;
+  double us;  // estimated time
 };
 W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms);
 // out[r] = a[rows[r]] for r < *last (clamped to [0, rows_max]); zeros where the

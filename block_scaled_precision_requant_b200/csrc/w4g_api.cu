@@ -136,34 +136,49 @@ bsr_status encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, u
   return BSR_OK;
 }
 
-// Few rows per expert: the decode kernel, which reads the weight once for up to
-// 16 rows; else the tensor-core kernel.
-bool few_rows(int64_t r, int64_t experts) { return r <= 16 * experts && r <= 4096; }
+// At most this many rows never take the tensor-core kernel.
+bool few_rows(int64_t r, int64_t experts) { return r <= 4 * experts; }
 
-// One product, every check and tensor map made before its launch.
+// One product, every check and tensor map made before its launch.  `gather`:
+// it takes its rows in order, from the buffer that the plan was given.
 struct Product {
   bsr::W4gArgs g;
-  bool few = false;
+  bool few = false, gather = false;
   bsr::W4gGemvPlan gemv;
   bsr::W4gGemmPlan gemm;
   CUtensorMap q, a;
 };
 
-bsr_status plan_product(Product& p, const bsr::W4gArgs& g, const Device& d) {
+bsr_status plan_product(Product& p, const bsr::W4gArgs& g, uint16_t* ordered, const Device& d) {
   p.g = g;
+  // The decode kernel reads the weight at more than the tensor-core kernel's
+  // rate and splits K, but its work grows with every 8 rows of an expert; the
+  // tensor-core kernel's time is that of whole tiles.  Each plan estimates its
+  // own.  (Measured, us, decode / tensor-core: 14336 x 4096 at 8 rows 16.8 /
+  // 17.3, at 12 32.8 / 17.3; 4096 x 4096 at 16 rows 11.2 / 19; 128 experts of
+  // 1536 x 2048 at 4 rows each 82 / 100, at 8 116 / 100.)
+  p.gemm = bsr::w4g_gemm_plan(g, d.num_sms);
   p.few = few_rows(g.rows_max, g.experts);
+  if (p.few || (g.rows_max <= 16LL * g.experts && g.rows_max <= 4096)) {
+    p.gemv = bsr::w4g_gemv_plan(g, d.num_sms);
+    p.few = p.few || p.gemv.us < p.gemm.us;
+  }
   const uint64_t wrows = (uint64_t)g.experts * (uint64_t)g.n, wpitch = (uint64_t)g.k / 2;
   if (p.few) {
-    p.gemv = bsr::w4g_gemv_plan(g, d.num_sms);
     return encode_2d(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, wpitch, wrows, wpitch, 128, (uint32_t)p.gemv.tr,
                      CU_TENSOR_MAP_SWIZZLE_128B, "w4g codes");
   }
-  p.gemm = bsr::w4g_gemm_plan(g, d.num_sms);
   const bsr_status st = encode_2d(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, wpitch, wrows, wpitch, 64, 128,
                                   CU_TENSOR_MAP_SWIZZLE_64B, "w4g codes");
   if (st != BSR_OK) return st;
-  return encode_2d(&p.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.a, (uint64_t)g.k, (uint64_t)g.a_rows, (uint64_t)g.k * 2,
-                   64, (uint32_t)p.gemm.bm, CU_TENSOR_MAP_SWIZZLE_128B, "w4g activations");
+  if (g.rows) {  // the tensor-core kernel takes its rows in order: they are gathered first
+    p.gather = true;
+    p.g.a = ordered;
+    p.g.a_rows = g.rows_max;
+    p.g.rows = nullptr;
+  }
+  return encode_2d(&p.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.g.a, (uint64_t)g.k, (uint64_t)p.g.a_rows,
+                   (uint64_t)g.k * 2, 64, (uint32_t)p.gemm.bm, CU_TENSOR_MAP_SWIZZLE_128B, "w4g activations");
 }
 
 bsr_status run_product(const Product& p, const Device& d, void* stream) {
@@ -240,7 +255,7 @@ bsr_status bsr_w4g_proj(const uint16_t* a, const bsr_w4g_weight* w, uint16_t* ou
   Device d;
   Product p;
   if ((st = device(d)) != BSR_OK) return st;
-  if ((st = plan_product(p, make_args(a, m, nullptr, nullptr, w, out, m, 1, n, k), d)) != BSR_OK) return st;
+  if ((st = plan_product(p, make_args(a, m, nullptr, nullptr, w, out, m, 1, n, k), nullptr, d)) != BSR_OK) return st;
   return run_product(p, d, stream);
 }
 
@@ -271,7 +286,6 @@ bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t
   if ((st = check_weight(w, "bsr_w4g_proj_grouped")) != BSR_OK) return st;
   if (!aligned(a, 16) || !aligned(out, 2) || !aligned(offsets, 4) || !aligned(rows, 4))
     return report(BSR_EALIGN, "bsr_w4g_proj_grouped: a must be 16-byte aligned, offsets and rows 4-byte, out 2-byte");
-  // the tensor-core kernel takes its rows in order: gather them first
   const size_t need = rows ? bsr_w4g_proj_grouped_scratch_bytes(r, experts, k) : 0;
   if (need && (!scratch || scratch_bytes < need))
     return report(BSR_ESCRATCH, "scratch of %zu bytes needed, %zu given", need, scratch ? scratch_bytes : (size_t)0);
@@ -280,14 +294,11 @@ bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t
   Product p;
   if ((st = device(d)) != BSR_OK) return st;
   uint16_t* ordered = static_cast<uint16_t*>(scratch);
-  if ((st = plan_product(p,
-                         need ? make_args(ordered, r, offsets, nullptr, w, out, r, experts, n, k)
-                              : make_args(a, a_rows, offsets, rows, w, out, r, experts, n, k),
-                         d)) != BSR_OK)
+  if ((st = plan_product(p, make_args(a, a_rows, offsets, rows, w, out, r, experts, n, k), ordered, d)) != BSR_OK)
     return st;
-  if (need && (st = cuda_status(bsr::launch_w4g_gather(a, a_rows, rows, offsets + experts, ordered, r, (int)k,
-                                                       as_stream(stream), d.num_sms),
-                                "row gather launch")) != BSR_OK)
+  if (p.gather && (st = cuda_status(bsr::launch_w4g_gather(a, a_rows, rows, offsets + experts, ordered, r, (int)k,
+                                                           as_stream(stream), d.num_sms),
+                                    "row gather launch")) != BSR_OK)
     return st;
   return run_product(p, d, stream);
 }
@@ -386,18 +397,16 @@ bsr_status bsr_w4g_moe_mlp(const uint16_t* x, const void* logits, int logits_typ
   uint16_t* u = reinterpret_cast<uint16_t*>(s + L.up);
   uint16_t* h = reinterpret_cast<uint16_t*>(s + L.hidden);
   uint16_t* y = reinterpret_cast<uint16_t*>(s + L.down);
-  // one gather serves gate and up
-  const bool gather = !few_rows(pairs, experts);
   uint16_t* ordered = reinterpret_cast<uint16_t*>(s + L.ordered);
-  const uint16_t* in = gather ? ordered : x;
-  const int64_t in_rows = gather ? pairs : tokens;
-  const int32_t* in_idx = gather ? nullptr : rows;
   Product pg, pu, pd;
-  if ((st = plan_product(pg, make_args(in, in_rows, offsets, in_idx, gate, g, pairs, experts, inner, k), d)) !=
+  if ((st = plan_product(pg, make_args(x, tokens, offsets, rows, gate, g, pairs, experts, inner, k), ordered, d)) !=
           BSR_OK ||
-      (st = plan_product(pu, make_args(in, in_rows, offsets, in_idx, up, u, pairs, experts, inner, k), d)) != BSR_OK ||
-      (st = plan_product(pd, make_args(h, pairs, offsets, nullptr, down, y, pairs, experts, k, inner), d)) != BSR_OK)
+      (st = plan_product(pu, make_args(x, tokens, offsets, rows, up, u, pairs, experts, inner, k), ordered, d)) !=
+          BSR_OK ||
+      (st = plan_product(pd, make_args(h, pairs, offsets, nullptr, down, y, pairs, experts, k, inner), nullptr, d)) !=
+          BSR_OK)
     return st;
+  const bool gather = pg.gather || pu.gather;  // once for both
   if ((st = bsr_moe_route(logits, logits_type, tokens, experts, top_k, flags, ids, weights, offsets, rows, pos,
                           s + L.route, L.ordered - L.route, stream)) != BSR_OK)
     return st;

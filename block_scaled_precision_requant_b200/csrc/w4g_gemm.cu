@@ -36,6 +36,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -683,25 +684,25 @@ cudaError_t launch_bm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4
 
 W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms) {
   W4gGemmPlan p = {};
-  const long long active = g.rows_max < g.experts ? g.rows_max : g.experts;
   const long long n_tiles = (g.n + kBn - 1) / kBn;
-  const long long rows = (g.rows_max + active - 1) / active;  // of an expert, on average
-  // Time of a tile by group (128, 64, 32) and width, relative: whole-kernel
-  // times of a 2048 x 14336 x 4096 product divided by its waves of tiles
-  // (100 = 10 us).
+  // Time of a tile at K = 4096 by width and group (128, 64, 32), us: a 2048 x
+  // 14336 x 4096 product divided by its waves of tiles.
   const int widths[4] = {192, 128, 64, 32};
-  const int tile_time[3][4] = {{215, 175, 161, 159}, {326, 246, 193, 172}, {513, 424, 338, 291}};
-  const int* time = tile_time[g.group == 128 ? 0 : g.group == 64 ? 1 : 2];
-  long long best = 0;
+  const double tile_us[3][4] = {{21.5, 16.7, 14.0, 13.5}, {25.5, 21.5, 17.1, 15.9}, {42.4, 35.2, 25.9, 24.1}};
+  const double* us = tile_us[g.group == 128 ? 0 : g.group == 64 ? 1 : 2];
+  const W4gSpread sp = w4g_spread(g);
   for (int i = 0; i < 4; ++i) {
-    const long long tiles = n_tiles * active * ((rows + widths[i] - 1) / widths[i]);
-    const long long cost = (tiles + num_sms - 1) / num_sms * time[i];
-    if (i == 0 || cost < best) {
-      best = cost;
+    const double waves = ceil((double)n_tiles * sp.tiles(widths[i]) / num_sms);
+    const double cost = waves * us[i] * ((double)g.k / 4096.0);
+    if (i == 0 || cost < p.us) {
+      p.us = cost;
       p.bm = widths[i];
     }
   }
-  const long long most = n_tiles * (active + g.rows_max / p.bm);  // of any grouping
+  p.us += 0.8;  // more to set up than the decode kernel
+  // of any grouping: each expert's last tile may be ragged
+  const long long most =
+      n_tiles * ((g.rows_max < g.experts ? g.rows_max : (long long)g.experts) + g.rows_max / p.bm);
   p.grid = (int)(most < num_sms ? most : num_sms);
   return p;
 }

@@ -566,14 +566,10 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   while (p.ks < kWarps && p.ks * 4 <= p.chunks) p.ks *= 2;
   const int ngrp = kWarps / p.ks;
   const int per_warp = (p.chunks + p.ks - 1) / p.ks;
-  // experts with rows, for choices without preference, and their items' rows
-  const double pairs = (double)g.rows_max, experts = (double)g.experts;
-  double active = g.experts == 1 ? 1.0 : experts * (1.0 - pow(1.0 - 1.0 / experts, pairs));
-  const double mean = pairs / active;
-  p.nt = mean <= 8.0 ? 1 : 2;
+  const W4gSpread sp = w4g_spread(g);
+  p.nt = sp.mean <= 8.0 ? 1 : 2;
   const int tok = 8 * p.nt;
-  const double tiles = g.experts == 1 ? (double)((g.rows_max + tok - 1) / tok)
-                                      : active * (mean <= 0.5 * tok ? 1.0 : 0.5 + mean / tok);
+  const double tiles = sp.tiles(tok);
   // rt tiles of tr rows per item: the least estimated time over whole waves
   // of two CTAs per SM.  Measured per wave: 2.3 us + 1.25 us per tile and
   // chunk of a warp (64 rows, K = 2048: 7.6 us; 16 rows: 3.5 us); tiles below
@@ -596,6 +592,9 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
     p.tr = atoi(getenv("W4G_RB")) % 100;
   }
 #endif
+  // two activation tiles cost more than twice one (registers); smaller groups
+  // carry more scales
+  p.us = best * 1.2 * (p.nt == 2 ? 2.2 : 1.0) * (g.group == 32 ? 1.35 : g.group == 64 ? 1.15 : 1.0);
   const int rb = p.rt * p.tr;
   p.nblk = (g.n + rb - 1) / rb;
   // slots: as many as leave room for two CTAs per SM (228 KB less 1 KB per

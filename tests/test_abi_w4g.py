@@ -66,7 +66,7 @@ def test_proj_grouped(L):
     assert call(w=weight(q=8)) == EALIGN and call(k=32) == ESHAPE
     assert call(a=None, off=None, rows=None, out=None, r=0) == OK
     # many rows per expert and a row index: the rows in group order
-    assert L.bsr_w4g_proj_grouped_scratch_bytes(32, 2, 64) == 0
+    assert L.bsr_w4g_proj_grouped_scratch_bytes(8, 2, 64) == 0
     need = L.bsr_w4g_proj_grouped_scratch_bytes(33, 2, 64)
     assert need == (33 * 64 * 2 + 255) // 256 * 256 and L.bsr_w4g_proj_grouped_scratch_bytes(-1, 2, 64) == 0
     assert call(r=33) == ESCRATCH and call(r=33, scratch=A, nbytes=need - 1) == ESCRATCH
