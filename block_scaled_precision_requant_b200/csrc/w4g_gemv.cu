@@ -57,12 +57,12 @@ struct GemvSmem {
   uint32_t meta, red, bars, off, pre, abort_flag, total;
 };
 
-// Per-warp ring of tile slots, per-warp scales of one tile and segment, the
-// warps' sums of an item, barriers, offsets and items before each expert.
+// Per-warp ring of tile slots, per-warp scales of a chunk, the warps' sums of
+// an item, barriers, offsets and items before each expert.
 __host__ __device__ inline GemvSmem gemv_smem(int rt, int nt, int group, int slots, int experts) {
   GemvSmem L;
   L.meta = kWarps * (uint32_t)slots * kSlotBytes;
-  L.red = L.meta + kWarps * (uint32_t)(kChunk / group / nt) * 8u * 16u;
+  L.red = L.meta + kWarps * (uint32_t)(kChunk / group) * (uint32_t)rt * 8u * 16u;
   L.bars = L.red + kWarps * (uint32_t)(rt * 16) * (uint32_t)(nt * 8) * 4u;
   L.off = L.bars + kWarps * (uint32_t)slots * 8u;
   L.pre = L.off + (uint32_t)(experts + 1) * 4u;
@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   constexpr int W = G / 32;                     // words per lane, row and group
   constexpr int GS = kChunk / G / NT;           // groups per segment
   constexpr int SEG = kChunk / NT;              // elements of K per segment
-  constexpr int LG = GS >= 2 ? GS / 2 : 1;      // groups whose scales one lane loads
+  constexpr int GC = kChunk / G;                // groups per chunk
+  constexpr int ML = (RT * 16 + 31) / 32;       // rows whose scales one lane loads
   constexpr int TOK = 8 * NT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L.abort_flag);
   uint8_t* ring = smem + (size_t)warp * (size_t)c.slots * kSlotBytes;
   const uint32_t ring_s = smem_u32(ring);
-  const uint32_t meta_s = smem_u32(smem) + L.meta + (uint32_t)warp * (uint32_t)GS * 128u;
+  const uint32_t meta_s = smem_u32(smem) + L.meta + (uint32_t)(warp * RT * GC) * 128u;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -302,54 +303,63 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         }
     return x;
   };
-  // Scales and zero points of one tile and segment: lane l has row l % 16,
-  // groups (l / 16) LG ...
-  const int mrow = lane & 15, mhalf = lane >> 4;
-  struct alignas(8) Meta {
-    alignas(8) uint16_t s[LG];
-    alignas(4) uint8_t z[LG];
+  // Scales and zero points of one chunk, as stored: lane l has rows l, l + 32 of
+  // the item's 16-row tiles.
+  struct alignas(16) Meta {
+    alignas(16) uint16_t s[ML][GC];
+    alignas(8) uint8_t z[ML][GC];
   };
-  auto load_meta = [&](const Item& t, int gi0, int i) {
+  auto load_meta = [&](const Item& t, int ch) {
     Meta m;
-    const int n = t.blk * rb + i * c.tr + mrow;
-    const int gi = gi0 + mhalf * LG;
-    const size_t at = ((size_t)t.e * g.n + n) * (size_t)groups + gi;
-    const bool row_ok = mrow < c.tr && n < g.n && mhalf * LG < GS;
+    const int gi = ch * GC;
 #pragma unroll
-    for (int v = 0; v < LG; ++v) {
-      m.s[v] = 0;
-      m.z[v] = 8;
-    }
-    if (LG > 1 && c.vec) {
-      if (row_ok && gi < groups) {
-        if constexpr (LG == 2) {
-          *reinterpret_cast<uint32_t*>(m.s) = *reinterpret_cast<const uint32_t*>(g.scale + at);
-          if (g.zero) *reinterpret_cast<uint16_t*>(m.z) = *reinterpret_cast<const uint16_t*>(g.zero + at);
-        } else if constexpr (LG == 4) {
-          *reinterpret_cast<uint2*>(m.s) = *reinterpret_cast<const uint2*>(g.scale + at);
-          if (g.zero) *reinterpret_cast<uint32_t*>(m.z) = *reinterpret_cast<const uint32_t*>(g.zero + at);
-        }
+    for (int l = 0; l < ML; ++l) {
+      const int tile = l * 2 + (lane >> 4), r = lane & 15;
+      const int n = t.blk * rb + tile * c.tr + r;
+      const bool ok = r < c.tr && tile < c.rt && n < g.n && gi < groups;
+      const size_t at = ((size_t)t.e * g.n + n) * (size_t)groups + gi;
+#pragma unroll
+      for (int v = 0; v < GC; ++v) {
+        m.s[l][v] = 0;
+        m.z[l][v] = 8;
       }
-    } else {
-#pragma unroll
-      for (int v = 0; v < LG; ++v)
-        if (row_ok && gi + v < groups) {
-          m.s[v] = g.scale[at + v];
-          if (g.zero) m.z[v] = g.zero[at + v];
+      if (c.vec) {
+        if (ok) {
+          if constexpr (GC == 2) {
+            *reinterpret_cast<uint32_t*>(m.s[l]) = __ldg(reinterpret_cast<const uint32_t*>(g.scale + at));
+            if (g.zero) *reinterpret_cast<uint16_t*>(m.z[l]) = __ldg(reinterpret_cast<const uint16_t*>(g.zero + at));
+          } else if constexpr (GC == 4) {
+            *reinterpret_cast<uint2*>(m.s[l]) = __ldg(reinterpret_cast<const uint2*>(g.scale + at));
+            if (g.zero) *reinterpret_cast<uint32_t*>(m.z[l]) = __ldg(reinterpret_cast<const uint32_t*>(g.zero + at));
+          } else {
+            *reinterpret_cast<uint4*>(m.s[l]) = __ldg(reinterpret_cast<const uint4*>(g.scale + at));
+            if (g.zero) *reinterpret_cast<uint2*>(m.z[l]) = __ldg(reinterpret_cast<const uint2*>(g.zero + at));
+          }
         }
+      } else {
+#pragma unroll
+        for (int v = 0; v < GC; ++v)
+          if (ok && gi + v < groups) {
+            m.s[l][v] = __ldg(g.scale + at + v);
+            if (g.zero) m.z[l][v] = __ldg(g.zero + at + v);
+          }
+      }
     }
     return m;
   };
-  // ... to shared memory, per group and mma row pair: {s(r), s(r + 8), -z/64
-  // of r, of r + 8}
+  // ... to shared memory, per tile, group and mma row pair: {s(r), s(r + 8),
+  // -z/64 of r, of r + 8}
+  const uint32_t meta_w =
+      meta_s + (uint32_t)(lane >> 4) * (GC * 128u) + (uint32_t)(lane & 7) * 16u + (uint32_t)((lane >> 3) & 1) * 4u;
   auto put_meta = [&](const Meta& m) {
-    if (mhalf * LG >= GS) return;
-    const uint32_t at = meta_s + (uint32_t)(mhalf * LG) * 128u + (uint32_t)(mrow & 7) * 16u + (uint32_t)(mrow >> 3) * 4u;
 #pragma unroll
-    for (int v = 0; v < LG; ++v) {
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 128u * v), "f"(scale_f32(m.s[v], g.half_scale)) : "memory");
-      if (g.zero) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 128u * v + 8u), "r"(zero_pair(m.z[v])) : "memory");
-    }
+    for (int l = 0; l < ML; ++l)
+#pragma unroll
+      for (int v = 0; v < GC; ++v) {
+        const uint32_t at = meta_w + (uint32_t)((l * 2 * GC + v) * 128);
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(scale_f32(m.s[l][v], g.half_scale)) : "memory");
+        if (g.zero) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 8u), "r"(zero_pair(m.z[l][v])) : "memory");
+      }
   };
 
   bool dead = false;
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   if (first < items) {
     next = find(first);
     next_index = index_of(next);
-    meta = load_meta(next, wk * GS * NT, 0);
+    meta = load_meta(next, wk);
   }
   int slot = 0;
   uint32_t phase = 0;
@@ -381,14 +391,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 
     for (int ch = wk; ch < c.chunks; ch += c.ks) {
       const bool last = ch + c.ks >= c.chunks;
+      __syncwarp();
+      put_meta(meta);
+      __syncwarp();
+      meta = load_meta(last ? next : t, last ? wk : ch + c.ks);
       const int slot0 = slot;  // the chunk's first tile
       const uint32_t phase0 = phase;
 #pragma unroll
       for (int seg = 0; seg < NT; ++seg) {
         const int gbase = (ch * NT + seg) * GS;
-        // where the next segment's scales are
-        const bool same = seg + 1 < NT || !last;
-        const int gnext = seg + 1 < NT ? gbase + GS : (last ? wk : ch + c.ks) * NT * GS;
         const Acts acts = load_acts(rows, gbase);
         uint32_t b[NT][GS][W][4];
 #pragma unroll
@@ -408,11 +419,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           if (i < c.rt) {
-            __syncwarp();
-            put_meta(meta);
-            __syncwarp();
-            const bool tile_last = i + 1 == c.rt;
-            meta = load_meta(tile_last && !same ? next : t, tile_last ? gnext : gbase, tile_last ? 0 : i + 1);
             if (seg == 0 && !dead) {
               const bool landed = mbar_wait(&bars[slot], phase, abort_flag, status, DEV_ERR_TIMEOUT_DECODE);
               if (__any_sync(0xFFFFFFFFu, !landed)) dead = true;
@@ -427,10 +433,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
               lds_words<W>(at + 8u * kChunkBytes, w1);
               float s0, s1;
               uint32_t z0 = 0xBE00BE00u, z1 = 0xBE00BE00u;  // -8 / 64
-              const uint32_t ma = meta_s + (uint32_t)gi * 128u + (uint32_t)r8 * 16u;
+              const uint32_t ma = meta_s + (uint32_t)((i * GC + seg * GS + gi) * 128) + (uint32_t)r8 * 16u;
               asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(s0), "=f"(s1) : "r"(ma));
               if (g.zero) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(z0), "=r"(z1) : "r"(ma + 8u));
-              float d[NT][4];
+              // two chains of products, so that one's latency passes during the other
+              float d[NT][2][4];
 #pragma unroll
               for (int w = 0; w < W; ++w) {
                 uint32_t p0[4], p1[4];
@@ -438,19 +445,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                 unpack8(w1[w], z1, p1);
 #pragma unroll
                 for (int tt = 0; tt < NT; ++tt) {
-                  if (w == 0)
-                    mma_bf16_first(d[tt], p0[0], p1[0], p0[1], p1[1], b[tt][gi][w][0], b[tt][gi][w][1]);
-                  else
-                    mma_bf16(d[tt], p0[0], p1[0], p0[1], p1[1], b[tt][gi][w][0], b[tt][gi][w][1]);
-                  mma_bf16(d[tt], p0[2], p1[2], p0[3], p1[3], b[tt][gi][w][2], b[tt][gi][w][3]);
+                  if (w == 0) {
+                    mma_bf16_first(d[tt][0], p0[0], p1[0], p0[1], p1[1], b[tt][gi][w][0], b[tt][gi][w][1]);
+                    mma_bf16_first(d[tt][1], p0[2], p1[2], p0[3], p1[3], b[tt][gi][w][2], b[tt][gi][w][3]);
+                  } else {
+                    mma_bf16(d[tt][0], p0[0], p1[0], p0[1], p1[1], b[tt][gi][w][0], b[tt][gi][w][1]);
+                    mma_bf16(d[tt][1], p0[2], p1[2], p0[3], p1[3], b[tt][gi][w][2], b[tt][gi][w][3]);
+                  }
                 }
               }
 #pragma unroll
               for (int tt = 0; tt < NT; ++tt) {
-                tot[i][tt][0] = fmaf(d[tt][0], s0, tot[i][tt][0]);
-                tot[i][tt][1] = fmaf(d[tt][1], s0, tot[i][tt][1]);
-                tot[i][tt][2] = fmaf(d[tt][2], s1, tot[i][tt][2]);
-                tot[i][tt][3] = fmaf(d[tt][3], s1, tot[i][tt][3]);
+                tot[i][tt][0] = fmaf(d[tt][0][0] + d[tt][1][0], s0, tot[i][tt][0]);
+                tot[i][tt][1] = fmaf(d[tt][0][1] + d[tt][1][1], s0, tot[i][tt][1]);
+                tot[i][tt][2] = fmaf(d[tt][0][2] + d[tt][1][2], s1, tot[i][tt][2]);
+                tot[i][tt][3] = fmaf(d[tt][0][3] + d[tt][1][3], s1, tot[i][tt][3]);
               }
             }
             if (++slot == c.slots) {
@@ -543,15 +552,16 @@ template <int G>
 cudaError_t launch_g(const CUtensorMap& tm, const W4gArgs& g, const W4gGemvPlan& p, int* status,
                      cudaStream_t stream) {
   GemvCfg c = {p.tr, p.rt, p.ks, p.slots, p.nblk, p.chunks, 0};
-  // a lane's scales start at a multiple of `lg` groups of its row
-  const int gs = kChunk / G / p.nt, lg = gs >= 2 ? gs / 2 : 1;
-  c.vec = (g.k / G) % lg == 0 && reinterpret_cast<uintptr_t>(g.scale) % (2u * lg) == 0 &&
-          reinterpret_cast<uintptr_t>(g.zero) % (unsigned)lg == 0;
-  if (p.rt <= 2)
-    return p.nt == 1 ? launch<G, 2, 1>(tm, g, c, p.grid, p.smem, status, stream)
-                     : launch<G, 2, 2>(tm, g, c, p.grid, p.smem, status, stream);
-  return p.nt == 1 ? launch<G, 4, 1>(tm, g, c, p.grid, p.smem, status, stream)
-                   : launch<G, 4, 2>(tm, g, c, p.grid, p.smem, status, stream);
+  constexpr int gc = kChunk / G;  // a chunk's scales start at a multiple of gc groups of the row
+  c.vec = (g.k / G) % gc == 0 && reinterpret_cast<uintptr_t>(g.scale) % (2u * gc) == 0 &&
+          reinterpret_cast<uintptr_t>(g.zero) % (unsigned)gc == 0;
+  if constexpr (G != 32) {  // at most two tiles there (see the plan)
+    if (p.rt > 2)
+      return p.nt == 1 ? launch<G, 4, 1>(tm, g, c, p.grid, p.smem, status, stream)
+                       : launch<G, 4, 2>(tm, g, c, p.grid, p.smem, status, stream);
+  }
+  return p.nt == 1 ? launch<G, 2, 1>(tm, g, c, p.grid, p.smem, status, stream)
+                   : launch<G, 2, 2>(tm, g, c, p.grid, p.smem, status, stream);
 }
 
 }  // namespace
@@ -576,7 +586,8 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   // 13 rows stream less but take as long.
   const double slots_all = 2.0 * num_sms * ngrp;
   double best = 0.0;
-  for (int rt = 4; rt >= 1; --rt)
+  // (At G = 32 four tiles' scales leave no room for a second CTA.)
+  for (int rt = g.group == 32 ? 2 : 4; rt >= 1; --rt)
     for (int tr = 16; tr >= 8; --tr) {
       const double items = (double)((g.n + rt * tr - 1) / (rt * tr)) * tiles;
       const double cost = ceil(items / slots_all) * (2.3 + per_warp * rt * 1.25 * (tr > 13 ? tr : 13) / 16.0);
@@ -598,10 +609,11 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   const int rb = p.rt * p.tr;
   p.nblk = (g.n + rb - 1) / rb;
   // slots: as many as leave room for two CTAs per SM (228 KB less 1 KB per
-  // CTA), at least one more than a chunk's tiles
+  // CTA).  A chunk's tiles stay until its last segment.
   const int rt_max = p.rt <= 2 ? 2 : 4;
+  const int least = p.nt == 1 ? 3 : p.rt + 1;
   p.slots = 6;
-  while (p.slots > p.rt + 1 && gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total > 115712u) --p.slots;
+  while (p.slots > least && gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total > 115712u) --p.slots;
   p.smem = gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total;
   // of any grouping: each expert's last tile may be ragged
   const long long items = (long long)p.nblk * ((g.rows_max < g.experts ? g.rows_max : g.experts) + g.rows_max / tok);
