@@ -814,10 +814,20 @@ def _like(t, name):
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return index, _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
+    return index, _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
-_HERE = contextlib.nullcontext()
+class _Here:
+    """The context that changes nothing."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
 
 
 def _ptr(t, dtype, shape, name, index):

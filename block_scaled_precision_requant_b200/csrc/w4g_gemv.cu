@@ -581,16 +581,18 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   const int tok = 8 * p.nt;
   const double tiles = sp.tiles(tok);
   // rt tiles of tr rows per item: the least estimated time over whole waves
-  // of two CTAs per SM.  Measured per wave: 2.3 us + 1.25 us per tile and
-  // chunk of a warp (64 rows, K = 2048: 7.6 us; 16 rows: 3.5 us); tiles below
-  // 13 rows stream less but take as long.
+  // of two CTAs per SM.  Measured per wave, us: 2.3, and per chunk of a warp
+  // 0.7 (its activations and scales) + 0.9 per tile (16 / 32 / 64 rows at K =
+  // 2048: 5.2 / 7.5 / 13.3, at K = 14336: 13.4 / 19 / 33).  A tile of fewer rows
+  // takes as long, so tr falls below 16 only where that saves a wave; three
+  // tiles take as long as four.
   const double slots_all = 2.0 * num_sms * ngrp;
   double best = 0.0;
   // (At G = 32 four tiles' scales leave no room for a second CTA.)
   for (int rt = g.group == 32 ? 2 : 4; rt >= 1; --rt)
     for (int tr = 16; tr >= 8; --tr) {
       const double items = (double)((g.n + rt * tr - 1) / (rt * tr)) * tiles;
-      const double cost = ceil(items / slots_all) * (2.3 + per_warp * rt * 1.25 * (tr > 13 ? tr : 13) / 16.0);
+      const double cost = ceil(items / slots_all) * (2.3 + per_warp * (0.7 + 0.9 * (rt == 3 ? 4 : rt)));
       if (best == 0.0 || cost < best - 1e-9) {
         best = cost;
         p.rt = rt;
@@ -603,9 +605,9 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
     p.tr = atoi(getenv("W4G_RB")) % 100;
   }
 #endif
-  // two activation tiles cost more than twice one (registers); smaller groups
+  // two activation tiles cost about twice one; smaller groups
   // carry more scales
-  p.us = best * 1.2 * (p.nt == 2 ? 2.2 : 1.0) * (g.group == 32 ? 1.35 : g.group == 64 ? 1.15 : 1.0);
+  p.us = best * 1.2 * (p.nt == 2 ? 1.8 : 1.0) * (g.group == 32 ? 1.35 : g.group == 64 ? 1.15 : 1.0);
   const int rb = p.rt * p.tr;
   p.nblk = (g.n + rb - 1) / rb;
   // slots: as many as leave room for two CTAs per SM (228 KB less 1 KB per
