@@ -34,13 +34,13 @@
 // wait that runs out sets a status bit and every role leaves its loop; copies
 // and MMAs in flight are drained (bounded) before the tensor memory is freed.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include <cmath>
 #include <mutex>
 
 #include "common.cuh"
 #include "w4g.h"
+#include "w4g_dev.cuh"
 
 namespace bsr {
 namespace {
@@ -143,27 +143,11 @@ __device__ __forceinline__ void regs_after_wait(uint32_t (&r)[R]) {
                       "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-
 // prmt, whose selectors with bit 3 set give a byte of copies of the sign bit.
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
   return d;
-}
-
-// The BF16 pair -z / 64.
-__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
-  const uint32_t h = __float_as_uint(-0.015625f * (float)z) & 0xFFFF0000u;
-  return h | (h >> 16);
-}
-
-__device__ __forceinline__ float scale_f32(uint16_t s, int half) {
-  return half ? __half2float(__ushort_as_half(s)) : __uint_as_float((uint32_t)s << 16);
 }
 
 // Bounded wait that ignores the abort flag (used while draining).
@@ -240,62 +224,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // tiles before each expert; the offsets clamped to [the one before, R]
-  if (warp == 0) {
-    int edge = 0, sum = 0;
-    const int rows_max = (int)g.rows_max;
-    for (int e0 = 0; e0 < g.experts; e0 += 32) {
-      const int e = e0 + lane;
-      int hi = 0;
-      if (e < g.experts) hi = g.offsets ? g.offsets[e + 1] : rows_max;
-      hi = min(max(hi, edge), rows_max);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, hi, o);
-        if (lane >= o) hi = max(hi, v);
-      }
-      int lo = __shfl_up_sync(0xFFFFFFFFu, hi, 1);
-      if (lane == 0) lo = edge;
-      int s = e < g.experts ? (int)(((unsigned)(hi - lo) + BM - 1) / BM) * n_tiles : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += v;
-      }
-      if (e < g.experts) {
-        s_off[e + 1] = hi;
-        s_pre[e + 1] = sum + s;
-      }
-      edge = __shfl_sync(0xFFFFFFFFu, hi, 31);
-      sum += __shfl_sync(0xFFFFFFFFu, s, 31);
-    }
-    if (lane == 0) s_off[0] = s_pre[0] = 0;
-  }
+  if (warp == 0) count_tiles(g, BM, n_tiles, lane, s_off, s_pre);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
   const int tiles = s_pre[g.experts];
   auto find = [&](int i) {
-    TileAt t;
-    int lo = 0, hi = g.experts;  // s_pre[lo] <= i < s_pre[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_pre[mid] <= i)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    t.e = lo;
-    const int rows = s_off[lo + 1] - s_off[lo];
-    const int m_tiles = (int)(((unsigned)rows + BM - 1) / BM);
-    const int local = i - s_pre[lo];
-    const int tn = local / m_tiles;
-    const int first = (local - tn * m_tiles) * BM;
-    t.n0 = tn * kBn;
-    t.row0 = s_off[lo] + first;
-    t.cnt = min(BM, rows - first);
-    return t;
+    const GroupTile f = find_tile(i, g.experts, BM, s_off, s_pre);
+    return TileAt{f.expert, f.n * kBn, f.row0, f.cnt};
   };
 
   if (warp < kDeqWarp0) {
@@ -444,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         z2 = zero_at(2);
       }
       for (int ks = 0; ks < kstages; ++ks, ++it) {
-        uint32_t zc[2] = {0xBE00BE00u, 0xBE00BE00u};  // -8 / 64
+        uint32_t zc[2] = {kZero8, kZero8};
         if (g.zero) {
           zc[0] = zero_pair(z0.a);
           zc[1] = G == 32 ? zero_pair(z0.b) : zc[0];
@@ -492,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               v[i * 4 + j] =
-                  fma_bf16x2(prmt(lo, hi, 0x8080u | (uint32_t)(j | (4 + j) << 8)), 0x7D007F00u, zc[hk]);
+                  fma_bf16x2(prmt(lo, hi, 0x8080u | (uint32_t)(j | (4 + j) << 8)), kLowHigh, zc[hk]);
           }
           tmem_st_x16(t_addr + (uint32_t)(ap.i * 64 + hk * 16), v);
         }

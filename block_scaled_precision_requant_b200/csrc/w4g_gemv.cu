@@ -28,16 +28,13 @@
 // the swizzle, the lanes of one shared-memory phase then hit distinct banks
 // for groups of 32, 64 and 128 (4, 8 and 16 bytes per lane).
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include <cmath>
-#ifdef W4G_FORCE
-#include <cstdlib>
-#endif
 #include <mutex>
 
 #include "common.cuh"
 #include "w4g.h"
+#include "w4g_dev.cuh"
 
 namespace bsr {
 namespace {
@@ -71,34 +68,14 @@ __host__ __device__ inline GemvSmem gemv_smem(int rt, int nt, int group, int slo
   return L;
 }
 
-__device__ __forceinline__ float scale_f32(uint16_t s, int half) {
-  return half ? __half2float(__ushort_as_half(s)) : __uint_as_float((uint32_t)s << 16);
-}
-
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-
-// 8 codes of a word -> four BF16 pairs ((q_j - z) / 64, (q_{j+4} - z) / 64),
-// exact; zc = the pair -z / 64.  Bits below 256 read as BF16 are that integer
-// times 2^-133 (subnormal below 128, the first normal binade above), so a
-// nibble in bits 0-3 or 4-7 of a half needs no shift and no exponent: the FMA
-// scales it by 2^127 or 2^123 and subtracts z.
+// 8 codes of a word -> four BF16 pairs ((q_j - z) / 64, (q_{j+4} - z) / 64);
+// zc = the pair -z / 64.
 __device__ __forceinline__ void unpack8(uint32_t w, uint32_t zc, uint32_t (&p)[4]) {
   const uint32_t v = w >> 8;
-  p[0] = fma_bf16x2(w & 0x000F000Fu, 0x7F007F00u, zc);
-  p[1] = fma_bf16x2(w & 0x00F000F0u, 0x7D007D00u, zc);
-  p[2] = fma_bf16x2(v & 0x000F000Fu, 0x7F007F00u, zc);
-  p[3] = fma_bf16x2(v & 0x00F000F0u, 0x7D007D00u, zc);
-}
-
-// The BF16 pair -z / 64.
-__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
-  const float f = -0.015625f * (float)z;
-  const uint32_t h = __float_as_uint(f) & 0xFFFF0000u;
-  return h | (h >> 16);
+  p[0] = fma_bf16x2(w & 0x000F000Fu, kLow2, zc);
+  p[1] = fma_bf16x2(w & 0x00F000F0u, kHigh2, zc);
+  p[2] = fma_bf16x2(v & 0x000F000Fu, kLow2, zc);
+  p[3] = fma_bf16x2(v & 0x00F000F0u, kHigh2, zc);
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -166,37 +143,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // items before each expert; the offsets clamped to [the one before, R]
-  if (warp == 0) {
-    int edge = 0, sum = 0;
-    for (int e0 = 0; e0 < g.experts; e0 += 32) {
-      const int e = e0 + lane;
-      int hi = 0;
-      if (e < g.experts) hi = g.offsets ? g.offsets[e + 1] : (int)g.rows_max;
-      hi = min(max(hi, edge), (int)g.rows_max);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, hi, o);
-        if (lane >= o) hi = max(hi, v);
-      }
-      int lo = __shfl_up_sync(0xFFFFFFFFu, hi, 1);
-      if (lane == 0) lo = edge;
-      const int items = e < g.experts ? (hi - lo + TOK - 1) / TOK * c.nblk : 0;
-      int s = items;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += v;
-      }
-      if (e < g.experts) {
-        s_off[e + 1] = hi;
-        s_pre[e + 1] = sum + s;
-      }
-      edge = __shfl_sync(0xFFFFFFFFu, hi, 31);
-      sum += __shfl_sync(0xFFFFFFFFu, s, 31);
-    }
-    if (lane == 0) s_off[0] = s_pre[0] = 0;
-  }
+  if (warp == 0) count_tiles(g, TOK, c.nblk, lane, s_off, s_pre);
   __syncthreads();
   const int items = s_pre[g.experts];
   const int step = (int)gridDim.x * ngrp;
@@ -204,28 +151,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   const int rb = c.tr * c.rt;  // weight rows of an item
 
   auto find = [&](int i) {
-    Item t;
-    int lo = 0, hi = g.experts;  // s_pre[lo] <= i < s_pre[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_pre[mid] <= i)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    t.e = lo;
-    const int rows = s_off[lo + 1] - s_off[lo];
-    const int local = i - s_pre[lo];
-    int tile = 0;
-    t.blk = local;
-    if (rows > TOK) {  // the tiles of one block are neighbours
-      const int tiles = (rows + TOK - 1) / TOK;
-      t.blk = local / tiles;
-      tile = local - t.blk * tiles;
-    }
-    t.row0 = s_off[lo] + tile * TOK;
-    t.cnt = min(TOK, rows - tile * TOK);
-    return t;
+    const GroupTile f = find_tile(i, g.experts, TOK, s_off, s_pre);
+    return Item{f.expert, f.n, f.row0, f.cnt};
   };
 
   // the warp's issue position: the next (item, chunk, tile) to request
@@ -432,7 +359,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
               lds_words<W>(at, w0);
               lds_words<W>(at + 8u * kChunkBytes, w1);
               float s0, s1;
-              uint32_t z0 = 0xBE00BE00u, z1 = 0xBE00BE00u;  // -8 / 64
+              uint32_t z0 = kZero8, z1 = kZero8;
               const uint32_t ma = meta_s + (uint32_t)((i * GC + seg * GS + gi) * 128) + (uint32_t)r8 * 16u;
               asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(s0), "=f"(s1) : "r"(ma));
               if (g.zero) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(z0), "=r"(z1) : "r"(ma + 8u));
@@ -599,12 +526,6 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
         p.tr = tr;
       }
     }
-#ifdef W4G_FORCE
-  if (getenv("W4G_RB")) {
-    p.rt = atoi(getenv("W4G_RB")) / 100;
-    p.tr = atoi(getenv("W4G_RB")) % 100;
-  }
-#endif
   // two activation tiles cost about twice one; smaller groups
   // carry more scales
   p.us = best * 1.2 * (p.nt == 2 ? 1.8 : 1.0) * (g.group == 32 ? 1.35 : g.group == 64 ? 1.15 : 1.0);

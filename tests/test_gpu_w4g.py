@@ -242,3 +242,119 @@ def test_empty_and_refusals():
         bsr.w4g_proj(a.half(), *w)
     with pytest.raises(bsr.BsrError, match="BSR_EALIGN"):
         bsr.w4g_proj(torch.zeros(4 * 64 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(4, 64), *w)
+
+
+def test_all_rows_of_one_of_many_experts():
+    """Groups unlike what the host expects: every row in the last expert, on
+    the decode kernel (4 rows per expert on average) and past it."""
+    n, k, group = 150, 320, 64
+    w = make_weight(23, (64,), n, k, group, True)
+    for r in (256, 1500):
+        a = make_acts(24, r, k)
+        off = offsets_of([0] * 63 + [r]).to(DEV)
+        out = bsr.w4g_proj_grouped(a.to(DEV), off, *dev(w))
+        ref, mag = reference(a, tuple(t[63] for t in w))
+        check(out, ref, mag, k, group)
+        # the first expert alone, the rest of the rows behind the last group
+        off = torch.full((65,), 5, dtype=torch.int32, device=DEV)
+        off[0] = 0
+        out = bsr.w4g_proj_grouped(a.to(DEV), off, *dev(w), out=torch.full((r, n), 2.0, dtype=torch.bfloat16,
+                                                                            device=DEV))
+        ref, mag = reference(a[:5], tuple(t[0] for t in w))
+        check(out[:5], ref, mag, k, group)
+        assert bool((out[5:] == 2.0).all())
+    assert bsr.device_status() == 0
+
+
+@pytest.mark.parametrize("m", [3, 40])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_scales_and_zero_points_at_any_alignment(m, group):
+    """Scales aligned to 2 bytes and zero points to 1, views into larger
+    buffers."""
+    n, k = 70, 1024
+    q, s, z = make_weight(25, (), n, k, group, True, True)
+    sb = torch.zeros(s.numel() + 3, dtype=s.dtype, device=DEV)[3:].view(s.shape).copy_(s)
+    zb = torch.zeros(z.numel() + 5, dtype=z.dtype, device=DEV)[5:].view(z.shape).copy_(z)
+    a = make_acts(26, m, k)
+    out = bsr.w4g_proj(a.to(DEV), q.to(DEV), sb, zb)
+    assert torch.equal(out, bsr.w4g_proj(a.to(DEV), q.to(DEV), s.to(DEV), z.to(DEV)))
+    ref, mag = reference(a, (q, s, z))
+    check(out, ref, mag, k, group)
+
+
+def test_magnitudes_of_activations():
+    """Activations from 2^-100 to 2^100 in one row, and outliers beside codes
+    at their zero point: the products are exact, so the bound holds as it is."""
+    n, k, group = 64, 512, 128
+    q, s, z = make_weight(27, (), n, k, group, True)
+    for m in (2, 40):
+        a = make_acts(28, m, k).double() * 2.0 ** torch.randint(-100, 101, (m, k), generator=torch.Generator().manual_seed(1))
+        a = a.bfloat16()
+        ref, mag = reference(a, (q, s, z))
+        check(bsr.w4g_proj(a.to(DEV), q.to(DEV), s.to(DEV), z.to(DEV)), ref, mag, k, group, "wide")
+        a = make_acts(29, m, k)
+        a[:, 7] = 2.0 ** 40
+        q2 = q.clone()
+        q2[:, 3] = (q2[:, 3] & 15) | (z[:, 0] << 4)  # element 7 at its zero point
+        ref, mag = reference(a, (q2, s, z))
+        check(bsr.w4g_proj(a.to(DEV), q2.to(DEV), s.to(DEV), z.to(DEV)), ref, mag, k, group, "outlier")
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first calls are captured, with nothing warmed up."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+import block_scaled_precision_requant_b200 as bsr
+torch.manual_seed(0)
+q = torch.randint(0, 256, (4, 256, 64), dtype=torch.uint8, device="cuda")
+s = torch.rand(4, 256, 1, device="cuda").bfloat16()
+d = torch.randint(0, 256, (4, 128, 128), dtype=torch.uint8, device="cuda")
+t = torch.rand(4, 128, 2, device="cuda").bfloat16()
+outs, ins = [], []
+g = torch.cuda.CUDAGraph()
+for m in (2, 90):
+    ins.append((torch.randn(m, 128, device="cuda").bfloat16(), torch.randn(m, 4, device="cuda")))
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    for x, lg in ins:
+        outs.append(bsr.w4g_moe_mlp(x, lg, (q, s, None), (q, s, None), (d, t, None), 2))
+        outs.append(bsr.w4g_proj(x, q[0], s[0]))
+g.replay()
+torch.cuda.synchronize()
+for i, (x, lg) in enumerate(ins):
+    assert torch.equal(outs[2 * i], bsr.w4g_moe_mlp(x, lg, (q, s, None), (q, s, None), (d, t, None), 2))
+    assert torch.equal(outs[2 * i + 1], bsr.w4g_proj(x, q[0], s[0]))
+assert bsr.device_status() == 0
+print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and p.stdout.strip().endswith("ok"), p.stderr[-2000:]
+
+
+def test_a_tensor_of_another_device_is_made_current(monkeypatch):
+    """Where the current device is another one, the call runs with the
+    tensor's device current and puts the old one back."""
+    w = dev(make_weight(30, (), 8, 64, 32))
+    a = make_acts(31, 4, 64).to(DEV)
+    want = bsr.w4g_proj(a, *w)
+    entered = []
+
+    class Guard:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append(self.index)
+
+        def __exit__(self, *exc):
+            entered.append("out")
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 5)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    assert torch.equal(bsr.w4g_proj(a, *w), want)
+    assert entered == [0, "out"]
