@@ -39,7 +39,13 @@
 namespace bsr {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;        // that multiply, after a warpgroup of which one warp requests the codes
+constexpr int kWarp0 = 4;
+constexpr int kThreads = 32 * (kWarp0 + kWarps);
+constexpr int kMaxSplit = 8;      // warps along K
+// register split: launched with 96 per thread
+constexpr int kLaunchRegs = 96, kCodesRegs = 24, kMulRegs = 112;
+static_assert(128 * kCodesRegs + 32 * kWarps * kMulRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kChunk = 256;       // elements of K per chunk
 constexpr int kChunkBytes = 128;  // of codes
 
@@ -61,7 +67,7 @@ __host__ __device__ inline GemvSmem gemv_smem(int rt, int nt, int group, int slo
   L.meta = kWarps * (uint32_t)slots * kSlotBytes;
   L.red = L.meta + kWarps * (uint32_t)(kChunk / group) * (uint32_t)rt * 8u * 16u;
   L.bars = L.red + kWarps * (uint32_t)(rt * 16) * (uint32_t)(nt * 8) * 4u;
-  L.off = L.bars + kWarps * (uint32_t)slots * 8u;
+  L.off = L.bars + kWarps * (uint32_t)slots * 16u;  // full and empty
   L.pre = L.off + (uint32_t)(experts + 1) * 4u;
   L.abort_flag = L.pre + (uint32_t)(experts + 1) * 4u;
   L.total = L.abort_flag + 16u + 1024u;  // 1 KB to align the slots
@@ -109,7 +115,7 @@ struct Item {
 
 // G: group.  RT: most 16-row tiles of an item.  NT: 8-row activation tiles.
 template <int G, int RT, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     w4g_gemv_kernel(const __grid_constant__ CUtensorMap tm_q, const W4gArgs g, const GemvCfg c,
                     int* __restrict__ status) {
   constexpr int W = G / 32;                     // words per lane, row and group
@@ -121,68 +127,83 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const GemvSmem L = gemv_smem(RT, NT, G, c.slots, g.experts);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int grp = warp / c.ks, wk = warp - grp * c.ks;
+  const int warp = (int)(threadIdx.x >> 5) - kWarp0, lane = threadIdx.x & 31;
   const int ngrp = kWarps / c.ks;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars) + (size_t)warp * c.slots;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);  // [warp][slot]
+  uint64_t* empty = full + (size_t)kWarps * c.slots;
   int* s_off = reinterpret_cast<int*>(smem + L.off);
   int* s_pre = reinterpret_cast<int*>(smem + L.pre);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L.abort_flag);
-  uint8_t* ring = smem + (size_t)warp * (size_t)c.slots * kSlotBytes;
-  const uint32_t ring_s = smem_u32(ring);
-  const uint32_t meta_s = smem_u32(smem) + L.meta + (uint32_t)(warp * RT * GC) * 128u;
 
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    tma_prefetch_desc(&tm_q);
-  }
-  if (lane == 0) {
-    for (int s = 0; s < c.slots; ++s) mbar_init(&bars[s], 1);
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (threadIdx.x < kWarps * c.slots) {
+    mbar_init(&full[threadIdx.x], 1);
+    mbar_init(&empty[threadIdx.x], 1);
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) tma_prefetch_desc(&tm_q);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp == 0) count_tiles(g, TOK, c.nblk, lane, s_off, s_pre);
+  if (warp == -kWarp0) count_tiles(g, TOK, c.nblk, lane, s_off, s_pre);
   __syncthreads();
   const int items = s_pre[g.experts];
   const int step = (int)gridDim.x * ngrp;
-  const int first = (int)blockIdx.x * ngrp + grp;
   const int rb = c.tr * c.rt;  // weight rows of an item
-
   auto find = [&](int i) {
     const GroupTile f = find_tile(i, g.experts, TOK, s_off, s_pre);
     return Item{f.expert, f.n, f.row0, f.cnt};
   };
 
-  // the warp's issue position: the next (item, chunk, tile) to request
-  int iss_item = first, iss_c = wk, iss_i = 0, iss_y = 0, iss_s = 0;
-  uint32_t issued = 0;
-  if (iss_item < items) {
-    const Item t = find(iss_item);
-    iss_y = t.e * g.n + t.blk * rb;
+  if (warp < 0) {
+    setmaxnreg_dec<kCodesRegs>();
+    if (warp != -kWarp0) return;
+    // ---------------------------------------------------------- codes
+    // lane w keeps warp w's ring full, across its chunks, tiles and items
+    const int grp = lane / c.ks, wk = lane - grp * c.ks;
+    uint64_t* f = full + lane * c.slots;
+    uint64_t* e = empty + lane * c.slots;
+    uint8_t* ring = smem + (size_t)lane * (size_t)c.slots * kSlotBytes;
+    int slot = 0;
+    uint32_t phase = 1, issued = 0;
+    bool ok = true;
+    if (lane < kWarps) {
+      for (int it = (int)blockIdx.x * ngrp + grp; ok && it < items; it += step) {
+        const Item t = find(it);
+        const int y = t.e * g.n + t.blk * rb;
+        for (int ch = wk; ok && ch < c.chunks; ch += c.ks)
+          for (int i = 0; i < c.rt; ++i) {
+            ok = mbar_wait(&e[slot], phase, abort_flag, status, DEV_ERR_TIMEOUT_DECODE);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&f[slot], (uint32_t)c.tr * kChunkBytes);
+            tma_load_2d(ring + (size_t)slot * kSlotBytes, &tm_q, &f[slot], ch * kChunkBytes, y + i * c.tr);
+            ++issued;
+            if (++slot == c.slots) {
+              slot = 0;
+              phase ^= 1u;
+            }
+          }
+      }
+      // after a wait that ran out, copies may be in flight that no warp waits
+      // for: wait here, again bounded, so the CTA does not exit under them
+      if (!ok) {
+        const unsigned long long t0 = globaltimer_ns();
+        const uint32_t n = (uint32_t)c.slots;
+        for (uint32_t j = issued > n ? issued - n : 0u; j < issued; ++j)
+          while (!mbar_try_wait(&f[j % n], (j / n) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
+          }
+      }
+    }
+    return;
   }
-  auto issue = [&]() {
-    if (iss_item >= items) return;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&bars[iss_s], (uint32_t)c.tr * kChunkBytes);
-      tma_load_2d(ring + (size_t)iss_s * kSlotBytes, &tm_q, &bars[iss_s], iss_c * kChunkBytes, iss_y + iss_i * c.tr);
-    }
-    ++issued;
-    if (++iss_s == c.slots) iss_s = 0;
-    if (++iss_i < c.rt) return;
-    iss_i = 0;
-    iss_c += c.ks;
-    if (iss_c < c.chunks) return;
-    iss_c = wk;
-    iss_item += step;
-    if (iss_item < items) {
-      const Item t = find(iss_item);
-      iss_y = t.e * g.n + t.blk * rb;
-    }
-  };
-  for (int s = 0; s < c.slots; ++s) issue();
+  setmaxnreg_inc<kMulRegs>();
 
+  const int grp = warp / c.ks, wk = warp - grp * c.ks;
+  const int first = (int)blockIdx.x * ngrp + grp;
+  uint64_t* bars = full + warp * c.slots;
+  uint64_t* released = empty + warp * c.slots;
+  const uint32_t ring_s = smem_u32(smem) + (uint32_t)(warp * c.slots * kSlotBytes);
+  const uint32_t meta_s = smem_u32(smem) + L.meta + (uint32_t)(warp * RT * GC) * 128u;
   const int t4 = lane & 3, g8 = lane >> 2;
   const int r8 = ((g8 & 1) << 2) | (g8 & 2) | (g8 >> 2);  // bit reversal
   const int groups = g.k / G;
@@ -236,15 +257,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     alignas(16) uint16_t s[ML][GC];
     alignas(8) uint8_t z[ML][GC];
   };
+  // this lane's rows within an item; groups are taken from the item's base
+  int mrow[ML];
+#pragma unroll
+  for (int l = 0; l < ML; ++l) {
+    const int tile = l * 2 + (lane >> 4), r = lane & 15;
+    mrow[l] = r < c.tr && tile < c.rt ? tile * c.tr + r : 1 << 30;
+  }
   auto load_meta = [&](const Item& t, int ch) {
     Meta m;
     const int gi = ch * GC;
+    const int left = g.n - t.blk * rb;  // rows of the item that exist
+    const size_t base = ((size_t)t.e * g.n + (size_t)t.blk * rb) * (size_t)groups + gi;
+    const uint16_t* sp = g.scale + base;
+    const uint8_t* zp = g.zero + base;
 #pragma unroll
     for (int l = 0; l < ML; ++l) {
-      const int tile = l * 2 + (lane >> 4), r = lane & 15;
-      const int n = t.blk * rb + tile * c.tr + r;
-      const bool ok = r < c.tr && tile < c.rt && n < g.n && gi < groups;
-      const size_t at = ((size_t)t.e * g.n + n) * (size_t)groups + gi;
+      const bool ok = mrow[l] < left;
+      const int at = mrow[l] * groups;
 #pragma unroll
       for (int v = 0; v < GC; ++v) {
         m.s[l][v] = 0;
@@ -253,22 +283,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       if (c.vec) {
         if (ok) {
           if constexpr (GC == 2) {
-            *reinterpret_cast<uint32_t*>(m.s[l]) = __ldg(reinterpret_cast<const uint32_t*>(g.scale + at));
-            if (g.zero) *reinterpret_cast<uint16_t*>(m.z[l]) = __ldg(reinterpret_cast<const uint16_t*>(g.zero + at));
+            *reinterpret_cast<uint32_t*>(m.s[l]) = __ldg(reinterpret_cast<const uint32_t*>(sp + at));
+            if (g.zero) *reinterpret_cast<uint16_t*>(m.z[l]) = __ldg(reinterpret_cast<const uint16_t*>(zp + at));
           } else if constexpr (GC == 4) {
-            *reinterpret_cast<uint2*>(m.s[l]) = __ldg(reinterpret_cast<const uint2*>(g.scale + at));
-            if (g.zero) *reinterpret_cast<uint32_t*>(m.z[l]) = __ldg(reinterpret_cast<const uint32_t*>(g.zero + at));
+            *reinterpret_cast<uint2*>(m.s[l]) = __ldg(reinterpret_cast<const uint2*>(sp + at));
+            if (g.zero) *reinterpret_cast<uint32_t*>(m.z[l]) = __ldg(reinterpret_cast<const uint32_t*>(zp + at));
           } else {
-            *reinterpret_cast<uint4*>(m.s[l]) = __ldg(reinterpret_cast<const uint4*>(g.scale + at));
-            if (g.zero) *reinterpret_cast<uint2*>(m.z[l]) = __ldg(reinterpret_cast<const uint2*>(g.zero + at));
+            *reinterpret_cast<uint4*>(m.s[l]) = __ldg(reinterpret_cast<const uint4*>(sp + at));
+            if (g.zero) *reinterpret_cast<uint2*>(m.z[l]) = __ldg(reinterpret_cast<const uint2*>(zp + at));
           }
         }
       } else {
 #pragma unroll
         for (int v = 0; v < GC; ++v)
           if (ok && gi + v < groups) {
-            m.s[l][v] = __ldg(g.scale + at + v);
-            if (g.zero) m.z[l][v] = __ldg(g.zero + at + v);
+            m.s[l][v] = __ldg(sp + at + v);
+            if (g.zero) m.z[l][v] = __ldg(zp + at + v);
           }
       }
     }
@@ -278,15 +308,30 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   // -z/64 of r, of r + 8}
   const uint32_t meta_w =
       meta_s + (uint32_t)(lane >> 4) * (GC * 128u) + (uint32_t)(lane & 7) * 16u + (uint32_t)((lane >> 3) & 1) * 4u;
+  auto put_scale = [&](uint32_t at, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(meta_w + at), "f"(v) : "memory");
+  };
   auto put_meta = [&](const Meta& m) {
+    if (g.half_scale) {
 #pragma unroll
-    for (int l = 0; l < ML; ++l)
+      for (int l = 0; l < ML; ++l)
 #pragma unroll
-      for (int v = 0; v < GC; ++v) {
-        const uint32_t at = meta_w + (uint32_t)((l * 2 * GC + v) * 128);
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(scale_f32(m.s[l][v], g.half_scale)) : "memory");
-        if (g.zero) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 8u), "r"(zero_pair(m.z[l][v])) : "memory");
-      }
+        for (int v = 0; v < GC; ++v) put_scale((uint32_t)((l * 2 * GC + v) * 128), scale_f32(m.s[l][v], 1));
+    } else {
+#pragma unroll
+      for (int l = 0; l < ML; ++l)
+#pragma unroll
+        for (int v = 0; v < GC; ++v) put_scale((uint32_t)((l * 2 * GC + v) * 128), scale_f32(m.s[l][v], 0));
+    }
+    if (g.zero) {
+#pragma unroll
+      for (int l = 0; l < ML; ++l)
+#pragma unroll
+        for (int v = 0; v < GC; ++v)
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta_w + (uint32_t)((l * 2 * GC + v) * 128 + 8)),
+                       "r"(zero_pair(m.z[l][v]))
+                       : "memory");
+    }
   };
 
   bool dead = false;
@@ -389,17 +434,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                 tot[i][tt][3] = fmaf(d[tt][0][3] + d[tt][1][3], s1, tot[i][tt][3]);
               }
             }
+            if (seg + 1 == NT) {  // every lane has read the slot: it may be refilled
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&released[slot]);
+            }
             if (++slot == c.slots) {
               slot = 0;
               phase ^= 1u;
-            }
-            if (seg + 1 == NT) {
-              // every lane has read the slot: it may be refilled (async proxy)
-              __syncwarp();
-              if (!dead) {
-                fence_proxy_async_smem();
-                issue();
-              }
             }
           }
         }
@@ -420,7 +461,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             mine[(tt * 8 + t4 * 2 + (j & 1)) * PITCH + i * 16 + (j >> 1) * 8 + r8] = tot[i][tt][j];
       }
     const int bar_threads = c.ks * 32;
-    asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(bar_threads) : "memory");
+    if (c.ks > 1)
+      asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(bar_threads) : "memory");
+    else
+      __syncwarp();
     const float* part = red + (size_t)grp * c.ks * PITCH * TOK;
     for (int i = wk * 32 + lane; i < PITCH * t.cnt; i += bar_threads) {
       const int tok = i / PITCH, r = i & (PITCH - 1);
@@ -431,15 +475,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       reinterpret_cast<__nv_bfloat16*>(g.out)[(size_t)(t.row0 + tok) * (size_t)g.n + row] =
           __float2bfloat16_rn(64.0f * v);
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(bar_threads) : "memory");
-  }
-  // a warp that gave up waiting may still have copies in flight: wait for
-  // them once more, again bounded, so the CTA does not exit under them
-  if (dead && lane == 0) {
-    const unsigned long long t0 = globaltimer_ns();
-    for (uint32_t j = issued > (uint32_t)c.slots ? issued - c.slots : 0u; j < issued; ++j)
-      while (!mbar_try_wait(&bars[j % c.slots], (j / c.slots) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
-      }
+    if (c.ks > 1)
+      asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(bar_threads) : "memory");
+    else
+      __syncwarp();
   }
 }
 
@@ -457,6 +496,10 @@ cudaError_t launch(const CUtensorMap& tm, const W4gArgs& g, const GemvCfg& c, in
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (smem > granted[dev]) {
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+      // the register split assumes every thread starts with kLaunchRegs registers
+      if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
       if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
         return e;
       granted[dev] = smem;
@@ -464,7 +507,7 @@ cudaError_t launch(const CUtensorMap& tm, const W4gArgs& g, const GemvCfg& c, in
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -483,9 +526,7 @@ cudaError_t launch_g(const CUtensorMap& tm, const W4gArgs& g, const W4gGemvPlan&
   c.vec = (g.k / G) % gc == 0 && reinterpret_cast<uintptr_t>(g.scale) % (2u * gc) == 0 &&
           reinterpret_cast<uintptr_t>(g.zero) % (unsigned)gc == 0;
   if constexpr (G != 32) {  // at most two tiles there (see the plan)
-    if (p.rt > 2)
-      return p.nt == 1 ? launch<G, 4, 1>(tm, g, c, p.grid, p.smem, status, stream)
-                       : launch<G, 4, 2>(tm, g, c, p.grid, p.smem, status, stream);
+    if (p.rt > 2) return launch<G, 4, 1>(tm, g, c, p.grid, p.smem, status, stream);
   }
   return p.nt == 1 ? launch<G, 2, 1>(tm, g, c, p.grid, p.smem, status, stream)
                    : launch<G, 2, 2>(tm, g, c, p.grid, p.smem, status, stream);
@@ -500,23 +541,23 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   // activations, the sum over warps) is that of two tiles' chunks.  By K only,
   // so that the order of a row's sum is.
   p.ks = 1;
-  while (p.ks < kWarps && p.ks * 4 <= p.chunks) p.ks *= 2;
+  while (p.ks < kMaxSplit && p.ks * 4 <= p.chunks) p.ks *= 2;
   const int ngrp = kWarps / p.ks;
   const int per_warp = (p.chunks + p.ks - 1) / p.ks;
   const W4gSpread sp = w4g_spread(g);
   p.nt = sp.mean <= 8.0 ? 1 : 2;
   const int tok = 8 * p.nt;
   const double tiles = sp.tiles(tok);
-  // rt tiles of tr rows per item: the least estimated time over whole waves
-  // of two CTAs per SM.  Measured per wave, us: 2.3, and per chunk of a warp
+  // rt tiles of tr rows per item: the least estimated time over whole waves.  Measured per wave, us: 2.3, and per chunk of a warp
   // 0.7 (its activations and scales) + 0.9 per tile (16 / 32 / 64 rows at K =
   // 2048: 5.2 / 7.5 / 13.3, at K = 14336: 13.4 / 19 / 33).  A tile of fewer rows
   // takes as long, so tr falls below 16 only where that saves a wave; three
   // tiles take as long as four.
-  const double slots_all = 2.0 * num_sms * ngrp;
+  const double slots_all = (double)num_sms * ngrp;
   double best = 0.0;
-  // (At G = 32 four tiles' scales leave no room for a second CTA.)
-  for (int rt = g.group == 32 ? 2 : 4; rt >= 1; --rt)
+  // (At G = 32 four tiles' scales, with two activation tiles their sums, leave
+  // too little room for the ring.)
+  for (int rt = g.group == 32 || p.nt == 2 ? 2 : 4; rt >= 1; --rt)
     for (int tr = 16; tr >= 8; --tr) {
       const double items = (double)((g.n + rt * tr - 1) / (rt * tr)) * tiles;
       const double cost = ceil(items / slots_all) * (2.3 + per_warp * (0.7 + 0.9 * (rt == 3 ? 4 : rt)));
@@ -531,17 +572,17 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   p.us = best * 1.2 * (p.nt == 2 ? 1.8 : 1.0) * (g.group == 32 ? 1.35 : g.group == 64 ? 1.15 : 1.0);
   const int rb = p.rt * p.tr;
   p.nblk = (g.n + rb - 1) / rb;
-  // slots: as many as leave room for two CTAs per SM (228 KB less 1 KB per
-  // CTA).  A chunk's tiles stay until its last segment.
+  // slots: as many as the shared memory of an SM (227 KB) has room for.  A
+  // chunk's tiles stay until its last segment.
   const int rt_max = p.rt <= 2 ? 2 : 4;
   const int least = p.nt == 1 ? 3 : p.rt + 1;
   p.slots = 6;
-  while (p.slots > least && gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total > 115712u) --p.slots;
+  while (p.slots > least && gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total > 232448u) --p.slots;
   p.smem = gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total;
   // of any grouping: each expert's last tile may be ragged
   const long long items = (long long)p.nblk * ((g.rows_max < g.experts ? g.rows_max : g.experts) + g.rows_max / tok);
   const long long ctas = (items + ngrp - 1) / ngrp;
-  p.grid = (int)(ctas < 2LL * num_sms ? ctas : 2LL * num_sms);
+  p.grid = (int)(ctas < num_sms ? ctas : num_sms);
   return p;
 }
 
