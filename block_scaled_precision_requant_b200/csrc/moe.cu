@@ -394,6 +394,8 @@ __global__ void __launch_bounds__(256)
                    int top_k, int n) {
   const int cols = n / VE;
   const long long items = tokens * cols;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += (long long)gridDim.x * 256) {
     const long long t = i / cols;
     const int c = (int)(i - t * cols);
@@ -443,9 +445,16 @@ cudaError_t launch_combine_v(const uint16_t* y, long long y_rows, const int32_t*
                              cudaStream_t stream, int num_sms) {
   const long long blocks = (tokens * (n / VE) + 255) / 256;
   const long long cap = (long long)num_sms * 8 * 64;
-  combine_kernel<VE><<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, stream>>>(y, y_rows, pos, weights, residual,
-                                                                                 out, tokens, top_k, n);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks < cap ? blocks : cap));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<VE>, y, y_rows, pos, weights, residual, out, tokens, top_k, n);
 }
 
 }  // namespace
