@@ -32,7 +32,6 @@ Integer 4-bit weights with group scales, and mixtures of experts over them:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Any, NamedTuple
@@ -805,15 +804,21 @@ def gemm_block_m(m: int, n: int) -> int:
 # worked out only when something is.
 
 
-def _like(t, name):
-    """(device index, context in which it is the current device) of the tensor
-    that fixes a call's device: the library launches on the current device."""
+def _like(t, name, stream):
+    """(device index, context of the call) of the tensor that fixes a call's
+    device.  In the context it is the current device, where the library
+    launches, and a given stream is the current stream, so that what the call
+    allocates belongs to the stream that uses it."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"{name} is on cuda:{index}, the stream on {stream.device}")
+        return index, torch.cuda.stream(stream)
     return index, _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
@@ -884,6 +889,8 @@ def _scratch(scratch, need, like):
         scratch = like.new_empty((need,), dtype=_torch().uint8)
     elif scratch.get_device() != like.get_device():
         raise ValueError(f"scratch must be on {like.device}")
+    elif not scratch.is_contiguous():
+        raise ValueError("scratch must be contiguous")
     return scratch.data_ptr(), scratch.numel() * scratch.element_size()
 
 
@@ -893,7 +900,7 @@ def w4g_proj(a, w_q, w_scale, w_zero=None, out=None, stream=None):
     low nibble of byte i), ``w_scale`` [N, K/G] bfloat16 or float16 with G =
     32, 64 or 128, ``w_zero`` [N, K/G] uint8 in 0..15 (None: 8)."""
     bf16 = _torch().bfloat16
-    index, here = _like(a, "a")
+    index, here = _like(a, "a", stream)
     m, k = _dims(a, 2, "a")
     n = _dims(w_q, 2, "w_q")[0]
     a_ptr = _ptr(a, bf16, (m, k), "a", index)
@@ -920,7 +927,7 @@ def w4g_proj_grouped(a, offsets, w_q, w_scale, w_zero=None, rows=None, out=None,
     (uninitialised when ``out`` is not given)."""
     torch = _torch()
     bf16 = torch.bfloat16
-    index, here = _like(a, "a")
+    index, here = _like(a, "a", stream)
     a_rows, k = _dims(a, 2, "a")
     experts, n = _dims(w_q, 3, "w_q")[:2]
     r = a_rows if rows is None else _dims(rows, 1, "rows")[0]
@@ -971,7 +978,7 @@ def moe_route(logits, top_k: int, renormalize: bool = True, stream=None) -> MoeR
     top_k = int(top_k)
     if not 1 <= top_k <= experts:
         raise ValueError(f"top_k must be in 1..{experts}, got {top_k}")
-    index, here = _like(logits, "logits")
+    index, here = _like(logits, "logits", stream)
     l_ptr = _ptr(logits, logits.dtype, (tokens, experts), "logits", index)
     with here:
         need = lib().bsr_moe_route_scratch_bytes(tokens, experts)
@@ -995,7 +1002,7 @@ def moe_combine(y, pos, weights, residual=None, out=None, stream=None):
     position outside [0, R) is skipped.  ``out`` may be ``residual``."""
     torch = _torch()
     bf16 = torch.bfloat16
-    index, here = _like(y, "y")
+    index, here = _like(y, "y", stream)
     r, n = _dims(y, 2, "y")
     tokens, top_k = pairs = _dims(pos, 2, "pos")
     y_ptr = _ptr(y, bf16, (r, n), "y", index)
@@ -1023,7 +1030,7 @@ def w4g_moe_mlp(x, logits, gate, up, down, top_k: int, renormalize: bool = True,
     :func:`w4g_proj_grouped`, :func:`silu_mul` and :func:`moe_combine` called
     one after the other."""
     bf16 = _torch().bfloat16
-    index, here = _like(x, "x")
+    index, here = _like(x, "x", stream)
     tokens, k = _dims(x, 2, "x")
     experts = _dims(logits, 2, "logits")[1]
     inner = _dims(gate[0], 3, "gate codes")[1]

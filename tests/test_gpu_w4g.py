@@ -358,3 +358,38 @@ def test_a_tensor_of_another_device_is_made_current(monkeypatch):
     monkeypatch.setattr(torch.cuda, "device", Guard)
     assert torch.equal(bsr.w4g_proj(a, *w), want)
     assert entered == [0, "out"]
+
+
+def test_given_stream_owns_what_the_call_allocates(monkeypatch):
+    """With ``stream=`` the scratch and outputs come from that stream's memory:
+    the current stream, which does not wait for it, is never handed them while
+    the call runs."""
+    g = torch.Generator(device=DEV).manual_seed(8)
+    experts, n, k, r = 4, 256, 512, 200
+    a = torch.randn(64, k, generator=g, device=DEV).to(torch.bfloat16)
+    off = torch.tensor([0, 60, 60, 150, 200], dtype=torch.int32, device=DEV)
+    rows = torch.randint(0, 64, (r,), generator=g, device=DEV, dtype=torch.int32)
+    q = torch.randint(0, 256, (experts, n, k // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s = torch.rand(experts, n, k // 64, generator=g, device=DEV).to(torch.bfloat16)
+    want = bsr.w4g_proj_grouped(a, off, q, s, rows=rows)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    seen = []
+    plain = bsr._scratch
+
+    def record(*args):
+        got = plain(*args)
+        seen.append(got)
+        return got
+
+    monkeypatch.setattr(bsr, "_scratch", record)
+    torch.cuda.empty_cache()
+    out = bsr.w4g_proj_grouped(a, off, q, s, rows=rows, stream=side)
+    (address, size), = seen
+    assert size > 0
+    held = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(3)]
+    assert address not in [t.data_ptr() for t in held]
+    side.synchronize()
+    assert torch.equal(out, want)
+    with pytest.raises(ValueError, match="contiguous"):
+        bsr.w4g_proj_grouped(a, off, q, s, rows=rows, scratch=torch.empty(2 * size, dtype=torch.uint8, device=DEV)[::2])
