@@ -60,7 +60,8 @@ bsr_status device(Device& out) {
   return BSR_OK;
 }
 
-bool dim_ok(int64_t x) { return x >= 0 && x <= BSR_MAX_DIM; }
+// The kernels count rows and elements of K in 32 bits, up to a tile past the end.
+bool dim_ok(int64_t x) { return x >= 0 && x <= BSR_W4G_MAX_DIM; }
 
 // Everything about a 4-bit weight that does not depend on its pointers.
 bsr_status check_format(const bsr_w4g_weight* w, const char* who, int64_t k) {
@@ -154,7 +155,8 @@ bsr_status plan_product(Product& p, const bsr::W4gArgs& g, uint16_t* ordered, co
   // The decode kernel reads the weight at more than the tensor-core kernel's
   // rate and splits K, but its work grows with every 8 rows of an expert; the
   // tensor-core kernel's time is that of whole tiles.  Each plan estimates its
-  // own.  (Measured, us, decode / tensor-core: 14336 x 4096 at 8 rows 16.8 /
+  // own, and past 16 rows per expert (two tiles of its widest item) or 4096 in
+  // all the decode kernel's never is the shorter.  (Measured, us, decode / tensor-core: 14336 x 4096 at 8 rows 16.8 /
   // 17.3, at 12 32.8 / 17.3; 4096 x 4096 at 16 rows 11.2 / 19; 128 experts of
   // 1536 x 2048 at 4 rows each 82 / 100, at 8 116 / 100.)
   p.gemm = bsr::w4g_gemm_plan(g, d.num_sms);
@@ -189,9 +191,9 @@ bsr_status run_product(const Product& p, const Device& d, void* stream) {
 
 bsr_status check_route_dims(const char* who, int64_t tokens, int64_t experts, int64_t top_k) {
   if (tokens < 0 || experts < 1 || experts > bsr::kRouteMaxExperts || top_k < 1 || top_k > experts ||
-      top_k > bsr::kRouteMaxTopK || tokens > BSR_MAX_DIM / top_k)
+      top_k > bsr::kRouteMaxTopK || tokens > BSR_W4G_MAX_DIM / top_k)
     return report(BSR_EINVAL, "%s: tokens=%lld experts=%lld top_k=%lld (1 <= experts <= %d, 1 <= top_k <= "
-                              "min(experts, %d), tokens * top_k < 2^31)",
+                              "min(experts, %d), tokens * top_k <= 2^31 - 256)",
                   who, (long long)tokens, (long long)experts, (long long)top_k, bsr::kRouteMaxExperts,
                   bsr::kRouteMaxTopK);
   return BSR_OK;
@@ -272,10 +274,10 @@ bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t
   bsr_status st = check_format(w, "bsr_w4g_proj_grouped", k);
   if (st != BSR_OK) return st;
   if (!dim_ok(a_rows) || !dim_ok(r) || !dim_ok(n) || !dim_ok(k) || experts < 1 || experts > bsr::kRouteMaxExperts ||
-      (n > 0 && experts > BSR_MAX_DIM / n))
+      (n > 0 && experts > BSR_W4G_MAX_DIM / n))
     return report(BSR_EINVAL,
                   "bsr_w4g_proj_grouped: dimension out of range (a_rows=%lld r=%lld experts=%lld n=%lld k=%lld; "
-                  "experts <= %d, experts * n < 2^31)",
+                  "experts <= %d, experts * n <= 2^31 - 256)",
                   (long long)a_rows, (long long)r, (long long)experts, (long long)n, (long long)k,
                   bsr::kRouteMaxExperts);
   if (r == 0 || n == 0) return ok();
@@ -336,7 +338,7 @@ bsr_status bsr_moe_combine(const uint16_t* y, int64_t y_rows, const int32_t* pos
                            const uint16_t* residual, uint16_t* out, int64_t tokens, int64_t top_k, int64_t n,
                            void* stream) {
   if (!dim_ok(y_rows) || !dim_ok(n) || tokens < 0 || top_k < 1 || top_k > bsr::kRouteMaxTopK ||
-      tokens > BSR_MAX_DIM / top_k)
+      tokens > BSR_W4G_MAX_DIM / top_k)
     return report(BSR_EINVAL, "bsr_moe_combine: dimension out of range (y_rows=%lld tokens=%lld top_k=%lld n=%lld)",
                   (long long)y_rows, (long long)tokens, (long long)top_k, (long long)n);
   if (tokens == 0 || n == 0) return ok();
@@ -353,7 +355,7 @@ bsr_status bsr_moe_combine(const uint16_t* y, int64_t y_rows, const int32_t* pos
 
 size_t bsr_w4g_moe_mlp_scratch_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner, int64_t k) {
   if (tokens <= 0 || experts < 1 || experts > bsr::kRouteMaxExperts || top_k < 1 || top_k > experts ||
-      top_k > bsr::kRouteMaxTopK || tokens > BSR_MAX_DIM / top_k || !dim_ok(inner) || !dim_ok(k) || inner == 0 ||
+      top_k > bsr::kRouteMaxTopK || tokens > BSR_W4G_MAX_DIM / top_k || !dim_ok(inner) || !dim_ok(k) || inner == 0 ||
       k == 0)
     return 0;
   return mlp_layout(tokens, experts, top_k, inner, k).total;
@@ -369,8 +371,8 @@ bsr_status bsr_w4g_moe_mlp(const uint16_t* x, const void* logits, int logits_typ
   if ((st = check_format(gate, who, k)) != BSR_OK || (st = check_format(up, who, k)) != BSR_OK ||
       (st = check_format(down, who, inner)) != BSR_OK)
     return st;
-  if (!dim_ok(inner) || !dim_ok(k) || experts > BSR_MAX_DIM / inner || experts > BSR_MAX_DIM / k)
-    return report(BSR_EINVAL, "%s: dimension out of range (inner=%lld k=%lld; experts times each < 2^31)", who,
+  if (!dim_ok(inner) || !dim_ok(k) || experts > BSR_W4G_MAX_DIM / inner || experts > BSR_W4G_MAX_DIM / k)
+    return report(BSR_EINVAL, "%s: dimension out of range (inner=%lld k=%lld; experts times each <= 2^31 - 256)", who,
                   (long long)inner, (long long)k);
   if (tokens == 0) return ok();
   if ((st = check_logits(who, logits, logits_type, flags)) != BSR_OK) return st;

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int l = 0; l < ML; ++l) {
       const bool ok = mrow[l] < left;
-      const int at = mrow[l] * groups;
+      const uint32_t at = (uint32_t)mrow[l] * (uint32_t)groups;  // below 64 x 2^26
 #pragma unroll
       for (int v = 0; v < GC; ++v) {
         m.s[l][v] = 0;

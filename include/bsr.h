@@ -428,7 +428,11 @@ bsr_status bsr_proj_silu(const uint16_t* gate, const uint16_t* up, const int8_t*
  *   W[n, k] = (q[n, k] - z[n, k / G]) * s[n, k / G],   G in {32, 64, 128}.
  * The experts' weights of one projection are stacked: codes [E, N, K/2],
  * scales [E, N, K/G], zero points [E, N, K/G].  Zero points above 15 are
- * outside the contract (results unspecified).
+ * outside the contract (results unspecified).  For given sizes, a call's output
+ * bits do not depend on scheduling; another number of rows may take another
+ * kernel, which adds the groups in another order.  Inputs, outputs and scratch
+ * must not overlap except where stated; calls that may run at the same time
+ * need scratch of their own.
  */
 #define BSR_W4G_SCALE_BF16 0
 #define BSR_W4G_SCALE_FP16 1
@@ -439,6 +443,10 @@ typedef struct bsr_w4g_weight {
   int scale_type;        /* BSR_W4G_SCALE_BF16 or BSR_W4G_SCALE_FP16 */
   int group;             /* G */
 } bsr_w4g_weight;
+
+/* Largest value of a dimension, of E * N and of T * top_k in these calls: the
+ * kernels count in 32 bits, up to a tile past the end. */
+#define BSR_W4G_MAX_DIM 2147483392LL
 
 /* Bounds of the expert operators. */
 #define BSR_MOE_MAX_EXPERTS 1024
@@ -463,9 +471,9 @@ bsr_status bsr_w4g_proj(const uint16_t* a, const bsr_w4g_weight* w, uint16_t* ou
  * as 0, each later offset is clamped to [the one before, R]; a row index
  * outside [0, a_rows) stands for a row of zeros.  Rows of out at or past
  * offsets[E] are left as they were.  1 <= E <= BSR_MOE_MAX_EXPERTS, E * N
- * below 2^31; shapes and alignment as bsr_w4g_proj.  Scratch (device, 256-byte
- * aligned) of bsr_w4g_proj_grouped_scratch_bytes(R, E, K), which holds the
- * rows in group order; none is needed (and 0 is returned) for few rows per
+ * at most BSR_W4G_MAX_DIM; shapes and alignment as bsr_w4g_proj.  Scratch
+ * (device, 256-byte aligned) of bsr_w4g_proj_grouped_scratch_bytes(R, E, K),
+ * which holds the rows in group order; none is needed (and 0 is returned) for few rows per
  * expert, nor when rows is NULL.
  */
 size_t bsr_w4g_proj_grouped_scratch_bytes(int64_t r, int64_t experts, int64_t k);
@@ -485,8 +493,9 @@ bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t
  *                        order, are rows offsets[e] .. offsets[e + 1] - 1
  *   rows    [T * top_k]  token of each grouped row; -1 past offsets[E]
  *   pos     [T, top_k]   grouped row of each pair, or -1 where id is -1
- * (A padded batch gives its padding tokens rows of -inf.)  T * top_k < 2^31,
- * top_k <= min(E, BSR_MOE_MAX_TOP_K), E <= BSR_MOE_MAX_EXPERTS.  T == 0
+ * (A padded batch gives its padding tokens rows of -inf.) 
+ * T * top_k <= BSR_W4G_MAX_DIM, top_k <= min(E, BSR_MOE_MAX_TOP_K), E <=
+ * BSR_MOE_MAX_EXPERTS.  T == 0
  * writes offsets only.  Scratch (device, 4-byte aligned) of
  * bsr_moe_route_scratch_bytes(T, E), which may be 0.  Results do not depend
  * on scheduling.

@@ -142,3 +142,25 @@ def test_binding_refuses_before_the_library():
                                 (4, torch.bfloat16, ValueError), (0, torch.bfloat16, ValueError)):
         with pytest.raises(error):
             bsr._w4g_weight(q, torch.zeros(8, groups, dtype=kind), None, (), 8, 64, -1, "w")
+
+
+def test_sizes_near_31_bits_are_refused(L):
+    """The kernels count rows and elements of K in 32 bits, up to a tile past
+    the end: 2^31 - 256 is the largest size."""
+    top = 2 ** 31 - 256
+    big = top + 32  # a multiple of 32
+    assert L.bsr_w4g_proj(A, weight(), A, 1, top + 1, 64, None) == EINVAL
+    assert L.bsr_w4g_proj(A, weight(), A, top + 1, 8, 64, None) == EINVAL
+    assert L.bsr_w4g_proj(A, weight(group=32), A, 1, 8, big, None) == EINVAL
+
+    def grouped(a_rows=4, r=4, e=2, n=8):
+        return L.bsr_w4g_proj_grouped(A, a_rows, A, A, weight(), A, r, e, n, 64, None, 0, None)
+
+    assert grouped(r=top + 1) == EINVAL and grouped(a_rows=top + 1) == EINVAL and grouped(n=2 ** 30 - 127) == EINVAL
+    assert "2^31 - 256" in bsr.last_error()
+    assert L.bsr_moe_route(A, 0, 2 ** 30 - 127, 8, 2, 0, A, A, A, A, A, None, 0, None) == EINVAL
+    assert L.bsr_moe_combine(A, 4, A, A, None, A, 2 ** 30 - 127, 2, 8, None) == EINVAL
+    assert L.bsr_moe_combine(A, top + 1, A, A, None, A, 4, 2, 8, None) == EINVAL
+    w = weight(group=32)
+    assert L.bsr_w4g_moe_mlp(A, A, 0, w, w, w, None, A, 4, 8, 2, 0, top // 8 + 32, 64, A, 0, None) == EINVAL
+    assert L.bsr_w4g_moe_mlp_scratch_bytes(4, 8, 2, big, 64) == 0
