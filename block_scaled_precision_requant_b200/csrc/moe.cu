@@ -69,8 +69,9 @@ struct RouteArgs {
 
 // The chosen experts of TP tokens t, t + step, ..., one step of each in turn so
 // that the warp reductions' latencies overlap: slot j's id and weight end in
-// lane j.  Each lane keeps its largest key and that key's expert; only the
-// lane whose expert was chosen looks through its keys again.
+// lane j.  Each lane keeps its largest key and that key's expert.  Up to four
+// keys are sorted once, so that the lane whose expert was chosen moves on to
+// its next; with more it looks through its keys again.
 template <int V, int TP>
 __device__ __forceinline__ void route_tokens(const RouteArgs& r, long long t, long long step, long long t1, int lane,
                                              int* hist) {
@@ -94,6 +95,32 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& r, long long t, lo
       key[p][v] = logit_key(x);
     }
   }
+  // keys in falling order and, in bytes from the lowest, their v
+  constexpr bool kSorted = V <= 4;
+  uint32_t order[TP];
+  auto sort_keys = [&](int p) {
+    uint32_t at[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) at[v] = (uint32_t)v;
+#pragma unroll
+    for (int end = V - 1; end > 0; --end)
+#pragma unroll
+      for (int v = 0; v < end; ++v) {  // neighbours, strictly: equal keys stay in order
+        const uint32_t a = key[p][v], b = key[p][v + 1], i = at[v], j = at[v + 1];
+        const bool swap = b > a;
+        key[p][v] = swap ? b : a;
+        key[p][v + 1] = swap ? a : b;
+        at[v] = swap ? j : i;
+        at[v + 1] = swap ? i : j;
+      }
+    order[p] = 0u;
+#pragma unroll
+    for (int v = 0; v < V && v < 4; ++v) order[p] |= at[v] << (8 * v);
+  };
+  auto head = [&](int p) {
+    best[p] = key[p][0];
+    best_at[p] = (order[p] & 0xFFu) * 32u + (unsigned)lane;
+  };
   auto rescan = [&](int p) {
     best[p] = key[p][V - 1];
     best_at[p] = (unsigned)((V - 1) * 32 + lane);
@@ -106,7 +133,12 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& r, long long t, lo
   };
 #pragma unroll
   for (int p = 0; p < TP; ++p) {
-    rescan(p);
+    if constexpr (kSorted) {
+      sort_keys(p);
+      head(p);
+    } else {
+      rescan(p);
+    }
     my_id[p] = -1;
     my_key[p] = 0u;
     top[p] = all[p] = 0.0f;
@@ -133,10 +165,18 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& r, long long t, lo
         my_key[p] = m[p];
       }
       if ((at[p] & 31u) == (unsigned)lane) {
+        if constexpr (kSorted) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if ((unsigned)(v * 32 + lane) == at[p]) key[p][v] = 0u;
-        rescan(p);
+          for (int v = 0; v + 1 < V; ++v) key[p][v] = key[p][v + 1];
+          key[p][V - 1] = 0u;
+          order[p] >>= 8;
+          head(p);
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if ((unsigned)(v * 32 + lane) == at[p]) key[p][v] = 0u;
+          rescan(p);
+        }
       }
     }
   }
