@@ -275,7 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (the unpacking warps waited for both), so that is the one wait.
       Pos p, ap, tp;
       bool ok = true;
-      constexpr uint32_t idesc = idesc_bf16(kBn, BM);
+      // a ragged tile multiplies its rows only, in whole steps of 16 (what the
+      // epilogue then reads past them it does not store)
+      uint32_t idesc = idesc_bf16(kBn, BM);
       const uint64_t b_desc0 = smem_desc_k_sw128(smem_u32(smem));
       // The MMAs of the stage's group `gi` (16 elements of K each) into the
       // current buffer and its commit; after the last group the stage's
@@ -301,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return !__any_sync(0xFFFFFFFFu, !in);
       };
       for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        idesc = idesc_bf16(kBn, (find(tile).cnt + 15) & ~15);
         for (int ks = 0; ks < kstages; ++ks) {
           const int count = min(kKs, g.k - ks * kKs) / G;  // groups of the stage
           if (!(ok = buffer_wait())) break;
