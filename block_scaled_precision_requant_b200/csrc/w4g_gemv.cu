@@ -311,6 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto put_scale = [&](uint32_t at, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(meta_w + at), "f"(v) : "memory");
   };
+  auto put_zero = [&](uint32_t at, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta_w + at + 8u), "r"(v) : "memory");
+  };
   auto put_meta = [&](const Meta& m) {
     if (g.half_scale) {
 #pragma unroll
@@ -327,12 +330,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int l = 0; l < ML; ++l)
 #pragma unroll
-        for (int v = 0; v < GC; ++v)
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta_w + (uint32_t)((l * 2 * GC + v) * 128 + 8)),
-                       "r"(zero_pair(m.z[l][v]))
-                       : "memory");
+        for (int v = 0; v < GC; ++v) put_zero((uint32_t)((l * 2 * GC + v) * 128), zero_pair(m.z[l][v]));
     }
   };
+  if (!g.zero) {  // the same for every chunk
+#pragma unroll
+    for (int l = 0; l < ML; ++l)
+#pragma unroll
+      for (int v = 0; v < GC; ++v) put_zero((uint32_t)((l * 2 * GC + v) * 128), kZero8);
+  }
 
   bool dead = false;
   Item next = {};
@@ -404,10 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               lds_words<W>(at, w0);
               lds_words<W>(at + 8u * kChunkBytes, w1);
               float s0, s1;
-              uint32_t z0 = kZero8, z1 = kZero8;
+              uint32_t z0, z1;
               const uint32_t ma = meta_s + (uint32_t)((i * GC + seg * GS + gi) * 128) + (uint32_t)r8 * 16u;
-              asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(s0), "=f"(s1) : "r"(ma));
-              if (g.zero) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(z0), "=r"(z1) : "r"(ma + 8u));
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=f"(s0), "=f"(s1), "=r"(z0), "=r"(z1) : "r"(ma));
               // two chains of products, so that one's latency passes during the other
               float d[NT][2][4];
 #pragma unroll
