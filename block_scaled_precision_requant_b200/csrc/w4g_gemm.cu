@@ -6,33 +6,45 @@
 // memory per group, one float32 FMA per element and group outside it.
 //
 // Tile: 128 weight rows (tensor-memory lanes, MMA M) x BM activation rows of
-// one expert (columns, MMA N).  The codes are the A operand and go through
-// tensor memory: a stage's codes (128 rows x 128 elements, 8 KB) come by TMA,
-// two sets of four warps unpack alternate stages to BF16 pairs (10
-// instructions per 8 elements) and store them with tcgen05.st as the A operand of `tcgen05.mma kind::f16`.
-// Through shared memory the unpacked tile (32 KB per stage, written once and
-// read once) would compete with the activation tile for its bandwidth.
-// Activations (B operand) come by TMA into 128-byte-swizzled tiles, so a row
-// index is resolved by a copy of the rows beforehand (w4g_gather_kernel): the
-// tile's rows gathered here measured 454 (TMA four-row gathers) and 284
-// (16-byte asynchronous copies of two warps) against 1040 TFLOP/s for tile
-// loads, while the copy is 2% of a product of 14336 weight rows.
+// one expert (columns, MMA N; a ragged tile multiplies its rows only).  The
+// codes are the A operand and go through tensor memory: a stage's codes (128
+// rows x 128 elements, 8 KB) come by TMA, eight warps unpack them to BF16
+// pairs (w4g_dev.cuh) and store them with tcgen05.st as the A operand of
+// `tcgen05.mma kind::f16`.  Through shared memory the unpacked tile (32 KB per
+// stage, written once and read once) would compete with the activation tile
+// for its bandwidth.  Activations (B operand) come by TMA into
+// 128-byte-swizzled tiles, so a row index is resolved by a copy of the rows
+// beforehand (w4g_gather_kernel): the tile's rows gathered here measured 454
+// (TMA four-row gathers) and 284 TFLOP/s (16-byte asynchronous copies of two
+// warps) against 1040 for tile loads, while the copy of 8192 rows of 4096 (23
+// us) is 3% of their product with 14336 weight rows.
 //
 // The scale changes every G elements of K, so each group accumulates into its
-// own tensor-memory buffer (a ring of 384 / BM) and the epilogue adds s * P
-// to float32 registers: a thread owns one weight row, so the scale is one
-// register, and BM / 2 columns.  Per SM and group that is 128 x BM FMAs (two
-// per instruction) against BM x G x 128 tensor FMAs: hidden for G = 64 and
-// 128; at G = 32 the unpacking and the rescale together fill the issue slots.
+// own tensor-memory buffer (two to six, what the unpacked stages leave of 512
+// columns) and the epilogue adds s * P to float32 registers: a thread owns one
+// weight row, so the scale is one register, and BM / 2 columns.  Per SM and
+// group that is 128 x BM FMAs (two per instruction) against BM x G x 128
+// tensor FMAs.
 //
 // Tiles are dealt to persistent CTAs in order of expert, weight tile,
 // activation tile (activation fastest, so that CTAs running together read the
 // same weight tile), from offsets read on the device.
 //
 // Warps (20): 0 TMA loads, 1 MMAs (one elected lane; owns the tensor memory),
-// 2-3 idle, 4-11 unpack (warp w: lanes 32 (w % 4)..), 12-19 epilogue (lanes 32 (w % 4).., column half).  Every wait is bounded: a
-// wait that runs out sets a status bit and every role leaves its loop; copies
-// and MMAs in flight are drained (bounded) before the tensor memory is freed.
+// 2-3 idle, 4-11 unpack (warp w: lanes 32 (w % 4).., half of each stage's K),
+// 12-19 epilogue (lanes 32 (w % 4).., half of the columns).  Every wait is
+// bounded: a wait that runs out sets a status bit and every role leaves its
+// loop; copies and MMAs in flight are drained (bounded) before the tensor
+// memory is freed.
+//
+// Measured, 2048 x 14336 x 4096: G = 128 192-199 us = 1210-1250 TFLOP/s (the
+// MMAs and the power limit: without the MMAs the rest takes 137 us), G = 64
+// 257 us = 940, G = 32 379 us = 635 TFLOP/s (a group's hand-over between MMA
+// and epilogue, about 520 cycles, and the FMAs).  Narrow tiles are bound by
+// the unpacking and the MMA warp's fixed work per group: 50 rows 18 us.
+// Tried and slower: 16 epilogue warps (G = 32 457 -> 620 us), two warps that
+// issue MMAs (190 -> 206); no faster: a third buffer at BM = 128, the
+// epilogue's loads a chunk ahead across groups.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -500,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < CW / 2; ++j)
-            acc[c][j] = __ffma2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2, acc[c][j]);
+            acc[c][j] =
+                __ffma2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2, acc[c][j]);
         }
         tp.next(C::TBUF);
       }

@@ -2,31 +2,49 @@
 //   out[r, n] = bf16( sum_g s[n, g] * sum_{k in g} a[r, k] * (q[n, k] - z[n, g]) )
 // on the weight as stored, rows grouped by expert (dense: one expert).
 //
-// Bound: the weight stream from HBM, half a byte per element, 46 elements per
-// SM and clock at the copy rate.  A CUDA-core FMA per element (after a
+// Bound: the weight stream from HBM, half a byte per element, is 46 elements
+// per SM and clock at the copy rate.  A CUDA-core FMA per element (after a
 // conversion) would need most of an SM's issue slots for one activation row
 // and more than all of them for several, so the products go through the
 // warp-level tensor instruction (mma.sync m16n8k16, BF16 -> F32): 16 weight
-// rows times up to 8 activation rows per instruction at the same cost for 1
-// row as for 8.  What is left on the CUDA cores is the unpacking, 11
-// instructions per 8 elements: shift and mask a pair of nibbles into the
-// mantissas of two BF16 values 128 + q, subtract 128 + z (both exact).  An
-// mma sums over K in any order, so nibble pairs (j, j + 4) of a 32-bit word
-// are taken as they come and the activations are permuted to match.  A
-// group's products are summed from zero by the mma, then scaled in float32.
+// rows times up to 8 activation rows per instruction, at the same cost for 1
+// row as for 8.  (tcgen05.mma wants 128 weight rows per tile and its operands
+// staged for one issuing thread; at 8 rows the staging is the work.)  What is
+// left on the CUDA cores is the unpacking: per word of 8 codes a shift, four
+// masks and four BF16-pair FMAs (w4g_dev.cuh).  An mma sums over K in any
+// order, so nibble pairs (j, j + 4) of a word are taken as they come and the
+// activations are permuted to match.  A group's products are summed from zero
+// by the mma, then scaled in float32.
 //
-// Work split: an item is `rb` weight rows (at most 16 RT) of one expert times
-// up to 8 NT of its activation rows; ks warps of a CTA split its K in chunks of
-// 256 (128 bytes) dealt cyclically, and add their sums in a fixed order
-// through shared memory.  The split depends on K only: a row's bits depend
-// neither on the other rows nor on the grid.  rb is chosen so that the items
-// fill whole waves of the resident CTAs.
+// Work split: an item is rt <= 4 tiles of tr <= 16 weight rows of one expert
+// times up to 8 NT of its activation rows; ks warps of a CTA split its K in
+// chunks of 256 (128 bytes) dealt cyclically, and add their sums in a fixed
+// order through shared memory.  The split depends on K only: a row's bits
+// depend neither on the other rows nor on the grid.  Larger items use an
+// activation load for more weight rows, smaller ones fill the last wave of
+// CTAs: the plan weighs the two by measured costs.
 //
-// Memory: each warp streams its chunks (rb rows x 128 bytes, 128-byte
-// swizzle) by TMA into its own ring of slots, issued ahead across items; no
-// CTA barrier in the stream.  Row g of an mma is slot row bitreverse3(g): with
-// the swizzle, the lanes of one shared-memory phase then hit distinct banks
-// for groups of 32, 64 and 128 (4, 8 and 16 bytes per lane).
+// One CTA per SM: 16 multiplying warps, and a producer warp whose lane w keeps
+// warp w's ring full of tiles (tr rows x 128 bytes, 128-byte swizzle, by TMA)
+// across chunks and items; no CTA barrier in the stream.  With the copies
+// issued by the multiplying warps themselves the same work took 17% longer (dense
+// 14336 x 4096, 1 row: 15.6 us against 13.3), and three or four smaller CTAs
+// per SM, which leave 56 to 72 registers per thread, spilled and took longer
+// still.  Row g of an mma is slot row bitreverse3(g): with the swizzle, the
+// lanes of one shared-memory phase then hit distinct banks for groups of 32,
+// 64 and 128 (4, 8 and 16 bytes per lane).  A chunk's scales and zero points
+// are read a chunk ahead and kept as stored until they are staged in shared
+// memory: converting them at the load would wait for it.
+//
+// Measured (inputs larger than L2): 14336 x 4096, groups of 128: 1 row 12.8
+// us = 2.4 TB/s, 8 rows 14.4 us; five or six experts of that size (4 tokens,
+// top 2 of 8) 45 us = 3.7 TB/s; 122 experts of 1536 x 2048 (48 tokens, top 8
+// of 128, groups of 64, zero points) 72.6 us = 2.9 TB/s.  With the
+// multiplication taken out the stream alone reaches 5.25 TB/s: the kernel is
+// bound by issue and instruction latency (about 21 instructions per word and
+// warp, 57% of the issue slots with 4 warps per scheduler; without the
+// unpacking's FMAs, 22% of all instructions, it is 9% faster), at one or two
+// waves also by the launch and the first bytes.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -39,8 +57,8 @@
 namespace bsr {
 namespace {
 
-constexpr int kWarps = 16;        // that multiply, after a warpgroup of which one warp requests the codes
-constexpr int kWarp0 = 4;
+constexpr int kWarps = 16;        // that multiply
+constexpr int kWarp0 = 4;         // the warps before them: one requests the codes
 constexpr int kThreads = 32 * (kWarp0 + kWarps);
 constexpr int kMaxSplit = 8;      // warps along K
 // register split: launched with 96 per thread
@@ -553,11 +571,11 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   p.nt = sp.mean <= 8.0 ? 1 : 2;
   const int tok = 8 * p.nt;
   const double tiles = sp.tiles(tok);
-  // rt tiles of tr rows per item: the least estimated time over whole waves.  Measured per wave, us: 2.3, and per chunk of a warp
-  // 0.7 (its activations and scales) + 0.9 per tile (16 / 32 / 64 rows at K =
-  // 2048: 5.2 / 7.5 / 13.3, at K = 14336: 13.4 / 19 / 33).  A tile of fewer rows
-  // takes as long, so tr falls below 16 only where that saves a wave; three
-  // tiles take as long as four.
+  // rt tiles of tr rows per item: the least estimated time over whole waves.
+  // Measured per wave, us: 2.3, and per chunk of a warp 0.7 (its activations and
+  // scales) + 0.9 per tile (16 / 32 / 64 rows at K = 2048: 5.2 / 7.5 / 13.3, at
+  // K = 14336: 13.4 / 19 / 33).  A tile of fewer rows takes as long, so tr falls
+  // below 16 only where that saves a wave; three tiles take as long as four.
   const double slots_all = (double)num_sms * ngrp;
   double best = 0.0;
   // (At G = 32 four tiles' scales, with two activation tiles their sums, leave
@@ -572,8 +590,7 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
         p.tr = tr;
       }
     }
-  // two activation tiles cost about twice one; smaller groups
-  // carry more scales
+  // two activation tiles cost about twice one; smaller groups carry more scales
   p.us = best * 1.2 * (p.nt == 2 ? 1.8 : 1.0) * (g.group == 32 ? 1.35 : g.group == 64 ? 1.15 : 1.0);
   const int rb = p.rt * p.tr;
   p.nblk = (g.n + rb - 1) / rb;
