@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 1, issued = 0;
     bool ok = true;
     if (lane < kWarps) {
-      for (int it = (int)blockIdx.x * ngrp + grp; ok && it < items; it += step) {
+      for (int it = grp * (int)gridDim.x + (int)blockIdx.x; ok && it < items; it += step) {
         const Item t = find(it);
         const int y = t.e * g.n + t.blk * rb;
         for (int ch = wk; ok && ch < c.chunks; ch += c.ks)
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   setmaxnreg_inc<kMulRegs>();
 
   const int grp = warp / c.ks, wk = warp - grp * c.ks;
-  const int first = (int)blockIdx.x * ngrp + grp;
+  const int first = grp * (int)gridDim.x + (int)blockIdx.x;
   uint64_t* bars = full + warp * c.slots;
   uint64_t* released = empty + warp * c.slots;
   const uint32_t ring_s = smem_u32(smem) + (uint32_t)(warp * c.slots * kSlotBytes);
@@ -603,8 +603,7 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   p.smem = gemv_smem(rt_max, p.nt, g.group, p.slots, g.experts).total;
   // of any grouping: each expert's last tile may be ragged
   const long long items = (long long)p.nblk * ((g.rows_max < g.experts ? g.rows_max : g.experts) + g.rows_max / tok);
-  const long long ctas = (items + ngrp - 1) / ngrp;
-  p.grid = (int)(ctas < num_sms ? ctas : num_sms);
+  p.grid = (int)(items < num_sms ? items : num_sms);
   return p;
 }
 
