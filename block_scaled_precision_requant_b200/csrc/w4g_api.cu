@@ -155,10 +155,13 @@ bsr_status plan_product(Product& p, const bsr::W4gArgs& g, uint16_t* ordered, co
   // The decode kernel reads the weight at more than the tensor-core kernel's
   // rate and splits K, but its work grows with every 8 rows of an expert; the
   // tensor-core kernel's time is that of whole tiles.  Each plan estimates its
-  // own, and past 16 rows per expert (two tiles of its widest item) or 4096 in
-  // all the decode kernel's never is the shorter.  (Measured, us, decode / tensor-core: 14336 x 4096 at 8 rows 16.8 /
-  // 17.3, at 12 32.8 / 17.3; 4096 x 4096 at 16 rows 11.2 / 19; 128 experts of
-  // 1536 x 2048 at 4 rows each 82 / 100, at 8 116 / 100.)
+  // own, and past 16 rows per expert (two tiles of the decode kernel's widest
+  // item) or 4096 in all its is never the shorter.  (Measured, us, decode /
+  // tensor-core: 14336 x 4096 at 8 rows 14.5 / 17.3, at 12 20.9 / 17.3, with
+  // groups of 32 26.9 / 27.5; 4096 x 4096 at 16 rows 10.9 / 16.4; 128 experts of
+  // 1536 x 2048 at 5 rows each 65 / 86, at 8 96 / 86, at 12 111 / 85, with groups
+  // of 32 144 / 151; 8 experts of 14336 x 4096 at 6 rows each 79 / 101, at 8 113 /
+  // 102.)
   p.gemm = bsr::w4g_gemm_plan(g, d.num_sms);
   p.few = few_rows(g.rows_max, g.experts);
   if (p.few || (g.rows_max <= 16LL * g.experts && g.rows_max <= 4096)) {

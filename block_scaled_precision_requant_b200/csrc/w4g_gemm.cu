@@ -646,13 +646,15 @@ W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms) {
   const W4gSpread sp = w4g_spread(g);
   for (int i = 0; i < 4; ++i) {
     const double waves = ceil((double)n_tiles * sp.tiles(widths[i]) / num_sms);
-    const double cost = waves * us[i] * ((double)g.k / 4096.0);
+    const double cost = waves * (0.6 + (us[i] - 0.6) * ((double)g.k / 4096.0));
     if (i == 0 || cost < p.us) {
       p.us = cost;
       p.bm = widths[i];
     }
   }
-  p.us += 0.8;  // more to set up than the decode kernel
+  // the launch and the set-up (50 rows of 14336 x 4096, one wave of 13.5: 17.3),
+  // and the copy of the rows
+  p.us += g.rows ? 5.5 : 3.0;
   // of any grouping: each expert's last tile may be ragged
   const long long most =
       n_tiles * ((g.rows_max < g.experts ? g.rows_max : (long long)g.experts) + g.rows_max / p.bm);

@@ -590,8 +590,11 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
         p.tr = tr;
       }
     }
-  // two activation tiles cost about twice one; smaller groups carry more scales
-  p.us = best * 1.2 * (p.nt == 2 ? 1.8 : 1.0) * (g.group == 32 ? 1.35 : g.group == 64 ? 1.15 : 1.0);
+  // The call: a launch, and by group and activation tiles (measured, us, 14336 x
+  // 4096, estimate before factors 10.9, at groups of 32 and two activation tiles
+  // 14.6: groups of 128 13.6, two tiles 21.0; 64 15.3 and 21.6; 32 17.5 and 27).
+  const double f = p.nt == 1 ? (g.group == 64 ? 1.15 : 1.0) : (g.group == 32 ? 1.65 : 1.25);
+  p.us = 2.7 + best * f;
   const int rb = p.rt * p.tr;
   p.nblk = (g.n + rb - 1) / rb;
   // slots: as many as the shared memory of an SM (227 KB) has room for.  A
