@@ -23,6 +23,9 @@
 // depend neither on the other rows nor on the grid.  Larger items use an
 // activation load for more weight rows, smaller ones fill the last wave of
 // CTAs: the plan weighs the two by measured costs.
+// Consecutive items go to different SMs, so that a partial last wave is
+// shared by all of them (64 tokens, top 8 of 128 experts of 1536 x 2048: 62.7
+// us; with a CTA's warps taking consecutive items 68.7).
 //
 // One CTA per SM: 16 multiplying warps, and a producer warp whose lane w keeps
 // warp w's ring full of tiles (tr rows x 128 bytes, 128-byte swizzle, by TMA)
@@ -36,10 +39,10 @@
 // are read a chunk ahead and kept as stored until they are staged in shared
 // memory: converting them at the load would wait for it.
 //
-// Measured (inputs larger than L2): 14336 x 4096, groups of 128: 1 row 12.8
-// us = 2.4 TB/s, 8 rows 14.4 us; five or six experts of that size (4 tokens,
-// top 2 of 8) 45 us = 3.7 TB/s; 122 experts of 1536 x 2048 (48 tokens, top 8
-// of 128, groups of 64, zero points) 72.6 us = 2.9 TB/s.  With the
+// Measured (inputs larger than L2): 14336 x 4096, groups of 128: 1 row 12.9
+// us = 2.3 TB/s, 8 rows 14.5 us; five or six experts of that size (4 tokens,
+// top 2 of 8) 44 us = 3.8 TB/s; 122 experts of 1536 x 2048 (48 tokens, top 8
+// of 128, groups of 64, zero points) 70.5 us = 3.0 TB/s.  With the
 // multiplication taken out the stream alone reaches 5.25 TB/s: the kernel is
 // bound by issue and instruction latency (about 21 instructions per word and
 // warp, 57% of the issue slots with 4 warps per scheduler; without the
