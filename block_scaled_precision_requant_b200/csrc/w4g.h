@@ -66,6 +66,7 @@ cudaError_t launch_w4g_gemv(const CUtensorMap& tm_q, const W4gArgs& g, const W4g
 // x 64, 128-byte swizzle.  Takes no row index.
 struct W4gGemmPlan {
   int bm, grid;
+  int split;  // CTAs (a cluster) that share the K of a tile; more than one only without offsets
   double us;  // estimated time
 };
 W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms);

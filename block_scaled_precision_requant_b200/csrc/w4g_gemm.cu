@@ -67,6 +67,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 12;
 constexpr size_t kSmemMax = 232448;
 constexpr int kLaunchRegs = 96, kCtrlRegs = 48;
+constexpr int kSumBytes = 160 * 1024;  // of any width's stages, for the sums of a cluster's other CTAs
 
 template <int BM>
 struct Cfg {
@@ -181,6 +182,11 @@ struct TileAt {
   int e, n0, row0, cnt;
 };
 
+// All threads of the cluster, from any place of the program.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Ring position.
 struct Pos {
   int i = 0;
@@ -196,7 +202,7 @@ struct Pos {
 template <int BM, int G>
 __global__ void __launch_bounds__(kThreads, 1)
     w4g_gemm_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_a,
-                    const W4gArgs g, const int stages, int* __restrict__ status) {
+                    const W4gArgs g, const int stages, const int split, int* __restrict__ status) {
   using C = Cfg<BM>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -209,7 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const int n_tiles = (g.n + kBn - 1) / kBn;
+  // K of this CTA: its share of the stages
   const int kstages = (g.k + kKs - 1) / kKs;
+  const int rank = (int)blockIdx.x % split;
+  const int ks0 = rank * kstages / split, ks1 = (rank + 1) * kstages / split;
+  const int first_tile = (int)blockIdx.x / split, tile_step = (int)gridDim.x / split;
   const int groups = g.k / G;
   // a stage: the activation tile, then the codes
   auto stage_ptr = [&](int s) { return smem + (size_t)s * C::STAGE; };
@@ -254,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       Pos p;
       uint32_t it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
         const TileAt t = find(tile);
-        for (int ks = 0; ks < kstages; ++ks) {
+        for (int ks = ks0; ks < ks1; ++ks) {
           ok = mbar_wait(&ctrl->empty[p.i], p.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_TMA);
           if (__any_sync(0xFFFFFFFFu, !ok)) {
             ok = false;
@@ -314,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool in = mbar_wait(&ctrl->tempty[tp.i], tp.phase ^ 1u, abort_flag, status, DEV_ERR_TIMEOUT_MMA);
         return !__any_sync(0xFFFFFFFFu, !in);
       };
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
         idesc = idesc_bf16(kBn, (find(tile).cnt + 15) & ~15);
-        for (int ks = 0; ks < kstages; ++ks) {
+        for (int ks = ks0; ks < ks1; ++ks) {
           const int count = min(kKs, g.k - ks * kKs) / G;  // groups of the stage
           if (!(ok = buffer_wait())) break;
           ok = mbar_wait(&ctrl->aready[ap.i], ap.phase, abort_flag, status, DEV_ERR_TIMEOUT_MMA);
@@ -370,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t it = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+    for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
       const uint8_t* zrow = nullptr;
       if (g.zero) {
         const TileAt t = find(tile);
@@ -391,11 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // of this and the next two stages
       Zeros z0 = {8, 8}, z1 = {8, 8}, z2 = {8, 8};
       if (g.zero) {
-        z0 = zero_at(0);
-        z1 = zero_at(1);
-        z2 = zero_at(2);
+        z0 = zero_at(ks0);
+        z1 = zero_at(ks0 + 1);
+        z2 = zero_at(ks0 + 2);
       }
-      for (int ks = 0; ks < kstages; ++ks, ++it) {
+      for (int ks = ks0; ks < ks1; ++ks, ++it) {
         uint32_t zc[2] = {kZero8, kZero8};
         if (g.zero) {
           zc[0] = zero_pair(z0.a);
@@ -469,24 +479,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     // conversion here would wait for the load)
     uint16_t sq[4];
     const uint16_t* srow = nullptr;
+    const int gi0 = ks0 * (kKs / G), gi1 = min(groups, ks1 * (kKs / G));
+    bool met = false;
     auto scale_at = [&](int gi) -> uint16_t { return srow && gi < groups ? __ldg(srow + gi) : (uint16_t)0; };
     auto open_tile = [&](const TileAt& t) {
       const int n = t.n0 + q * 32 + lane;
       srow = n < g.n ? g.scale + ((size_t)t.e * g.n + n) * (size_t)groups : nullptr;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sq[i] = scale_at(i);
+      for (int i = 0; i < 4; ++i) sq[i] = scale_at(gi0 + i);
     };
     TileAt t = {};
-    if ((int)blockIdx.x < tiles) {
-      t = find(blockIdx.x);
+    if (first_tile < tiles) {
+      t = find(first_tile);
       open_tile(t);
     }
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+    for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < CW / 2; ++j) acc[c][j] = make_float2(0.0f, 0.0f);
-      for (int gi = 0; gi < groups; ++gi) {
+      for (int gi = gi0; gi < gi1; ++gi) {
         const float sc = scale_f32(sq[0], g.half_scale);
         const float2 s2 = make_float2(sc, sc);
         sq[0] = sq[1];
@@ -517,10 +529,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tp.next(C::TBUF);
       }
+      if (split > 1) {
+        // The first CTA adds the others' sums, in their order, from its own
+        // stages' memory, which nothing uses once all are here.  (A cluster has
+        // one tile; after an abort too its CTAs meet.)
+        met = true;
+        constexpr uint32_t kPart = (uint32_t)BM * 128u * 4u;
+        const uint32_t mine = (uint32_t)((h * C::COLS) * 128 + q * 32 + lane) * 4u;
+        cluster_meet();
+        if (rank > 0) {
+          uint32_t at;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+                       : "=r"(at)
+                       : "r"(smem_u32(smem) + (uint32_t)(rank - 1) * kPart + mine));
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < CW; ++j)
+              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + (uint32_t)(c * CW + j) * 512u),
+                           "f"((j & 1) ? acc[c][j >> 1].y : acc[c][j >> 1].x)
+                           : "memory");
+        }
+        cluster_meet();
+        if (rank > 0) break;
+        for (int r = 0; r + 1 < split; ++r) {
+          const float* part = reinterpret_cast<const float*>(smem + (size_t)r * kPart + mine);
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < CW / 2; ++j) {
+              acc[c][j].x += part[(c * CW + 2 * j) * 128];
+              acc[c][j].y += part[(c * CW + 2 * j + 1) * 128];
+            }
+        }
+      }
       if (!ok) break;
       const TileAt now = t;
-      if (tile + (int)gridDim.x < tiles) {  // the next tile's scales are on their way during the stores
-        t = find(tile + gridDim.x);
+      if (tile + tile_step < tiles) {  // the next tile's scales are on their way during the stores
+        t = find(tile + tile_step);
         open_tile(t);
       }
       const int n = now.n0 + q * 32 + lane;
@@ -537,7 +583,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       }
       __syncwarp();
+      if (split > 1) break;
     }
+    if (split > 1 && !met) {
+      cluster_meet();
+      cluster_meet();
+    }
+  }
+  if (split > 1 && warp < kEpiWarp0) {  // with the epilogue's two meetings
+    __syncwarp();
+    cluster_meet();
+    cluster_meet();
   }
 
   tc_fence_before();
@@ -588,8 +644,8 @@ int stage_count(int experts) {
 std::mutex g_mu;
 
 template <int BM, int G>
-cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, int grid, int* status,
-                   cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,
+                   int* status, cudaStream_t stream) {
   auto kern = w4g_gemm_kernel<BM, G>;
   static bool granted[64] = {};
   int dev = 0;
@@ -610,25 +666,28 @@ cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gAr
   }
   const int stages = stage_count<BM>(g.experts);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes<BM>(stages, g.experts);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm_q, tm_a, g, stages, status);
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_q, tm_a, g, stages, p.split, status);
 }
 
 template <int BM>
-cudaError_t launch_bm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, int grid, int* status,
-                      cudaStream_t stream) {
+cudaError_t launch_bm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,
+                      int* status, cudaStream_t stream) {
   switch (g.group) {
-    case 32: return launch<BM, 32>(tm_q, tm_a, g, grid, status, stream);
-    case 64: return launch<BM, 64>(tm_q, tm_a, g, grid, status, stream);
-    case 128: return launch<BM, 128>(tm_q, tm_a, g, grid, status, stream);
+    case 32: return launch<BM, 32>(tm_q, tm_a, g, p, status, stream);
+    case 64: return launch<BM, 64>(tm_q, tm_a, g, p, status, stream);
+    case 128: return launch<BM, 128>(tm_q, tm_a, g, p, status, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -644,12 +703,28 @@ W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms) {
   const double tile_us[3][4] = {{21.5, 16.7, 14.0, 13.5}, {25.5, 21.5, 17.1, 15.9}, {42.4, 35.2, 25.9, 24.1}};
   const double* us = tile_us[g.group == 128 ? 0 : g.group == 64 ? 1 : 2];
   const W4gSpread sp = w4g_spread(g);
+  const int kstages = (g.k + kKs - 1) / kKs;
+  p.split = 1;
   for (int i = 0; i < 4; ++i) {
-    const double waves = ceil((double)n_tiles * sp.tiles(widths[i]) / num_sms);
-    const double cost = waves * (0.6 + (us[i] - 0.6) * ((double)g.k / 4096.0));
-    if (i == 0 || cost < p.us) {
-      p.us = cost;
+    const double tiles = (double)n_tiles * sp.tiles(widths[i]);
+    const auto cost = [&](int split) {
+      return ceil(tiles * split / num_sms) * (0.6 + (us[i] - 0.6) * ((double)g.k / split / 4096.0));
+    };
+    if (i == 0 || cost(1) < p.us) {
+      p.us = cost(1);
       p.bm = widths[i];
+      p.split = 1;
+    }
+    // Few tiles of a dense product: clusters share their K, where it has work
+    // for all and the first CTA's stages hold the others' sums.
+    for (int split = 2; split <= 8 && !g.offsets; split *= 2) {
+      if (tiles * split > num_sms || kstages < 4 * split || (split - 1) * widths[i] * 512 > kSumBytes) break;
+      const double us_split = cost(split) + 1.5;
+      if (us_split < p.us) {
+        p.us = us_split;
+        p.bm = widths[i];
+        p.split = split;
+      }
     }
   }
   // the launch and the set-up (50 rows of 14336 x 4096, one wave of 13.5: 17.3),
@@ -659,6 +734,7 @@ W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms) {
   const long long most =
       n_tiles * ((g.rows_max < g.experts ? g.rows_max : (long long)g.experts) + g.rows_max / p.bm);
   p.grid = (int)(most < num_sms ? most : num_sms);
+  if (p.split > 1) p.grid = p.split * (int)(n_tiles * ((g.rows_max + p.bm - 1) / p.bm));
   return p;
 }
 
@@ -683,10 +759,10 @@ cudaError_t launch_w4g_gather(const uint16_t* a, long long a_rows, const int32_t
 cudaError_t launch_w4g_gemm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,
                             int* status, cudaStream_t stream) {
   switch (p.bm) {
-    case 32: return launch_bm<32>(tm_q, tm_a, g, p.grid, status, stream);
-    case 64: return launch_bm<64>(tm_q, tm_a, g, p.grid, status, stream);
-    case 128: return launch_bm<128>(tm_q, tm_a, g, p.grid, status, stream);
-    case 192: return launch_bm<192>(tm_q, tm_a, g, p.grid, status, stream);
+    case 32: return launch_bm<32>(tm_q, tm_a, g, p, status, stream);
+    case 64: return launch_bm<64>(tm_q, tm_a, g, p, status, stream);
+    case 128: return launch_bm<128>(tm_q, tm_a, g, p, status, stream);
+    case 192: return launch_bm<192>(tm_q, tm_a, g, p, status, stream);
     default: return cudaErrorInvalidValue;
   }
 }
