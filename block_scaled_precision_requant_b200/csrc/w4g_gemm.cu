@@ -30,6 +30,11 @@
 // activation tile (activation fastest, so that CTAs running together read the
 // same weight tile), from offsets read on the device.
 //
+// A dense product of few tiles leaves most SMs without one; clusters of 2, 4 or
+// 8 CTAs then share a tile's K, and the first adds the others' float32 sums, in
+// their order, from its own shared memory (17 rows of 4096 x 4096: 16.2 us with
+// 32 CTAs, 9.1 with clusters of 4; 64 rows of 4096 x 14336: 49.9 and 19.5).
+//
 // Warps (20): 0 TMA loads, 1 MMAs (one elected lane; owns the tensor memory),
 // 2-3 idle, 4-11 unpack (warp w: lanes 32 (w % 4).., half of each stage's K),
 // 12-19 epilogue (lanes 32 (w % 4).., half of the columns).  Every wait is
@@ -692,6 +697,39 @@ cudaError_t launch_bm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4
   }
 }
 
+// Clusters of `split` CTAs that the current device runs at once: a cluster lies
+// within one group of SMs, so that of 148 SMs 33 clusters of 4 and 15 of 8 were
+// found to fit (one more takes a second wave: 4736 weight rows in 37 clusters of
+// 4 16.0 us, 4224 in 33 9.2).
+int cluster_room(int split) {
+  static int room[64][9] = {};  // + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lk(g_mu);
+  int& r = room[dev][split];
+  if (r == 0) {
+    auto kern = w4g_gemm_kernel<32, 128>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemMax;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // answered by not splitting
+      n = 0;
+    }
+    r = n + 1;
+  }
+  return r - 1;
+}
+
 }  // namespace
 
 W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms) {
@@ -716,9 +754,12 @@ W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms) {
       p.split = 1;
     }
     // Few tiles of a dense product: clusters share their K, where it has work
-    // for all and the first CTA's stages hold the others' sums.
+    // for all, the first CTA's stages hold the others' sums and all clusters run
+    // at once.  1.5: the two meetings and the sums.
     for (int split = 2; split <= 8 && !g.offsets; split *= 2) {
-      if (tiles * split > num_sms || kstages < 4 * split || (split - 1) * widths[i] * 512 > kSumBytes) break;
+      if (tiles * split > num_sms || kstages < 4 * split || (split - 1) * widths[i] * 512 > kSumBytes ||
+          tiles > cluster_room(split))
+        break;
       const double us_split = cost(split) + 1.5;
       if (us_split < p.us) {
         p.us = us_split;

@@ -3,7 +3,7 @@ float64 oracle.
 
 Tolerance, per output: the result is rounded once to BF16 (at most 2^-8 of the
 value) from float32 sums of exact products.  A group's sum has G terms and an
-output adds K/G scaled groups plus at most 16 partial sums of warps; each
+output adds K/G scaled groups plus at most 16 partial sums of warps or CTAs; each
 addition is off by at most 2^-23 (a tensor-core addition may truncate) and
 each scaling by 2^-24 of the sum of magnitudes S, hence
 |err| <= 2^-8 |ref| + (1 + 2^-8) (G + K/G + 18) 2^-23 S."""
@@ -393,3 +393,70 @@ def test_given_stream_owns_what_the_call_allocates(monkeypatch):
     assert torch.equal(out, want)
     with pytest.raises(ValueError, match="contiguous"):
         bsr.w4g_proj_grouped(a, off, q, s, rows=rows, scratch=torch.empty(2 * size, dtype=torch.uint8, device=DEV)[::2])
+
+
+SHARED_K = [
+    # few tiles and a K of at least eight stages of 128: two, four or eight CTAs per tile
+    (17, 1, 1024, 128), (33, 300, 2080, 32), (17, 1000, 4160, 64), (50, 1920, 4096, 128), (100, 77, 4256, 32),
+    (130, 513, 1152, 128), (192, 129, 8192, 64), (300, 1024, 1088, 64), (200, 2300, 2048, 128), (17, 4700, 2048, 32),
+]
+
+
+@pytest.mark.parametrize("zero,half", [(False, True), (True, False)])
+@pytest.mark.parametrize("m,n,k,group", SHARED_K)
+def test_dense_with_k_shared_by_a_cluster(m, n, k, group, zero, half):
+    w = make_weight(m + n + k, (), n, k, group, zero, half)
+    a = make_acts(n, m, k)
+    x, wd = a.to(DEV), dev(w)
+    out = bsr.w4g_proj(x, *wd)
+    ref, mag = reference(a, w)
+    check(out, ref, mag, k, group)
+    guard = torch.full((m + 2, n), 7.0, device=DEV, dtype=torch.bfloat16)
+    for _ in range(3):
+        bsr.w4g_proj(x, *wd, out=guard[1:-1])
+        assert torch.equal(guard[1:-1], out)
+    assert bool((guard[0] == 7.0).all()) and bool((guard[-1] == 7.0).all())
+    assert bsr.device_status() == 0
+
+
+def test_shared_k_back_to_back_on_two_streams():
+    """Launches whose clusters follow or meet one another: the same bits."""
+    w = make_weight(5, (), 2048, 4096, 64, True, False)
+    wd = dev(w)
+    xs = [make_acts(i, m, 4096).to(DEV) for i, m in enumerate((17, 100, 64, 33))]
+    want = [bsr.w4g_proj(x, *wd) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for r in range(10):
+        for i, x in enumerate(xs):
+            got.append((i, bsr.w4g_proj(x, *wd, stream=streams[(r + i) % 2])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in got)
+    assert bsr.device_status() == 0
+
+
+def test_first_shared_k_call_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+import block_scaled_precision_requant_b200 as bsr
+torch.manual_seed(0)
+q = torch.randint(0, 256, (512, 1024), dtype=torch.uint8, device="cuda")
+s = torch.rand(512, 32, device="cuda").bfloat16()
+x = torch.randn(40, 2048, device="cuda").bfloat16()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = bsr.w4g_proj(x, q, s)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, bsr.w4g_proj(x, q, s)) and bsr.device_status() == 0
+print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and p.stdout.strip().endswith("ok"), p.stderr[-2000:]
