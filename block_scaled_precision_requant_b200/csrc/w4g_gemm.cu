@@ -44,12 +44,13 @@
 //
 // Measured, 2048 x 14336 x 4096: G = 128 192-199 us = 1210-1250 TFLOP/s (the
 // MMAs and the power limit: without the MMAs the rest takes 137 us), G = 64
-// 257 us = 940, G = 32 379 us = 635 TFLOP/s (a group's hand-over between MMA
-// and epilogue, about 520 cycles, and the FMAs).  Narrow tiles are bound by
-// the unpacking and the MMA warp's fixed work per group: 50 rows 18 us.
-// Tried and slower: 16 epilogue warps (G = 32 457 -> 620 us), two warps that
-// issue MMAs (190 -> 206); no faster: a third buffer at BM = 128, the
-// epilogue's loads a chunk ahead across groups.
+// 229-257 us = 940-1050, G = 32 365-379 us = 635-660 TFLOP/s (the epilogue's
+// chain of wait, load and FMAs per group, about 520 cycles; no pipe is above
+// 42%).  Narrow tiles are bound by the unpacking and the MMA warp's fixed work
+// per group: 50 rows 17 us.  Tried and slower: 16 epilogue warps (G = 32 457 ->
+// 620 us), two warps that issue MMAs (190 -> 206); no faster: a third buffer at
+// BM = 128, the epilogue's loads a chunk ahead within a group (more than 16
+// columns of them spill) or across groups.
 #include <cuda_bf16.h>
 
 #include <cmath>
