@@ -983,13 +983,18 @@ def moe_route(logits, top_k: int, renormalize: bool = True, stream=None) -> MoeR
     with here:
         need = lib().bsr_moe_route_scratch_bytes(tokens, experts)
         scratch = logits.new_empty((need,), dtype=torch.uint8) if need else None
-        ids = logits.new_empty((tokens, top_k), dtype=torch.int32)
-        weights = torch.empty_like(ids, dtype=torch.float32)
-        offsets = ids.new_empty((experts + 1,))
-        rows = ids.new_empty((tokens * top_k,))
-        pos = torch.empty_like(ids)
-        _check(lib().bsr_moe_route(l_ptr, kind, tokens, experts, top_k, 1 if renormalize else 0, ids.data_ptr(),
-                                   weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
+        # one allocation, whose parts the results are
+        pairs = tokens * top_k
+        table, step = (tokens, top_k), (top_k, 1)
+        parts = logits.new_empty((4 * pairs + experts + 1,), dtype=torch.int32)
+        ids = torch.as_strided(parts, table, step, 0)
+        weights = torch.as_strided(parts.view(torch.float32), table, step, pairs)
+        pos = torch.as_strided(parts, table, step, 2 * pairs)
+        rows = torch.as_strided(parts, (pairs,), (1,), 3 * pairs)
+        offsets = torch.as_strided(parts, (experts + 1,), (1,), 4 * pairs)
+        at, size = parts.data_ptr(), 4 * pairs
+        _check(lib().bsr_moe_route(l_ptr, kind, tokens, experts, top_k, 1 if renormalize else 0, at, at + size,
+                                   at + 4 * size, at + 3 * size, at + 2 * size,
                                    None if scratch is None else scratch.data_ptr(), need,
                                    _raw_stream(stream, index)))
     return MoeRoute(ids, weights, offsets, rows, pos)
