@@ -12,7 +12,8 @@ namespace bsr {
 
 // One product over weight rows stacked by expert (dense: one expert, no
 // offsets).  Row r of the output, off[e] <= r < off[e + 1], is row rows[r] of
-// a (r itself when rows is null) times expert e's weight.
+// a (r itself when rows is null) times expert e's weight; off[0] = 0 and off[e]
+// = min(max(off[e - 1], offsets[e]), rows_max).
 struct W4gArgs {
   const uint16_t* a;       // [a_rows, K] BF16
   const int32_t* offsets;  // [experts + 1], or null: one expert with `rows_max` rows
@@ -70,10 +71,11 @@ struct W4gGemmPlan {
   double us;  // estimated time
 };
 W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms);
-// out[r] = a[rows[r]] for r < *last (clamped to [0, rows_max]); zeros where the
-// index is outside a.  16-byte aligned rows.
-cudaError_t launch_w4g_gather(const uint16_t* a, long long a_rows, const int32_t* rows, const int32_t* last,
-                              uint16_t* out, long long rows_max, int k, cudaStream_t stream, int num_sms);
+// out[r] = a[rows[r]] for the rows of all groups (offsets as in W4gArgs, clamped
+// alike); zeros where the index is outside a.  16-byte aligned rows.
+cudaError_t launch_w4g_gather(const uint16_t* a, long long a_rows, const int32_t* rows, const int32_t* offsets,
+                              int experts, uint16_t* out, long long rows_max, int k, cudaStream_t stream,
+                              int num_sms);
 cudaError_t launch_w4g_gemm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,
                             int* status, cudaStream_t stream);
 

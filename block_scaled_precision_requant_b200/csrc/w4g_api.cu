@@ -301,7 +301,7 @@ bsr_status bsr_w4g_proj_grouped(const uint16_t* a, int64_t a_rows, const int32_t
   uint16_t* ordered = static_cast<uint16_t*>(scratch);
   if ((st = plan_product(p, make_args(a, a_rows, offsets, rows, w, out, r, experts, n, k), ordered, d)) != BSR_OK)
     return st;
-  if (p.gather && (st = cuda_status(bsr::launch_w4g_gather(a, a_rows, rows, offsets + experts, ordered, r, (int)k,
+  if (p.gather && (st = cuda_status(bsr::launch_w4g_gather(a, a_rows, rows, offsets, (int)experts, ordered, r, (int)k,
                                                            as_stream(stream), d.num_sms),
                                     "row gather launch")) != BSR_OK)
     return st;
@@ -415,7 +415,7 @@ bsr_status bsr_w4g_moe_mlp(const uint16_t* x, const void* logits, int logits_typ
   if ((st = bsr_moe_route(logits, logits_type, tokens, experts, top_k, flags, ids, weights, offsets, rows, pos,
                           s + L.route, L.ordered - L.route, stream)) != BSR_OK)
     return st;
-  if (gather && (st = cuda_status(bsr::launch_w4g_gather(x, tokens, rows, offsets + experts, ordered, pairs, (int)k,
+  if (gather && (st = cuda_status(bsr::launch_w4g_gather(x, tokens, rows, offsets, (int)experts, ordered, pairs, (int)k,
                                                          as_stream(stream), d.num_sms),
                                   "row gather launch")) != BSR_OK)
     return st;

@@ -609,13 +609,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Rows of a, by index, in the order of the groups: 16 bytes per thread.  An
-// index outside a gives a row of zeros; rows past the last group are left.
+// index outside a gives a row of zeros; rows past the last group are left.  The
+// last group ends where count_tiles lets it end, at the largest offset: one that
+// falls stands for the one before it.  (Each warp reads all offsets, which costs
+// nothing that shows: a call of 8192 rows of 4096 of 128 experts, 128 weight rows
+// each, 46.4 us with and without, of 8192 rows of 256 of 1024 experts 29.3.)
 __global__ void __launch_bounds__(256) w4g_gather_kernel(const uint4* __restrict__ a, const int32_t* __restrict__ rows,
-                                                         const int32_t* __restrict__ last, uint4* __restrict__ out,
-                                                         int rows_max, int a_rows, int cols) {
+                                                         const int32_t* __restrict__ offsets, uint4* __restrict__ out,
+                                                         int rows_max, int a_rows, int experts, int cols) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long items = (long long)min(max(__ldg(last), 0), rows_max) * cols;
+  int last = 0;
+#pragma unroll 4
+  for (int e = 1 + (threadIdx.x & 31); e <= experts; e += 32) last = max(last, __ldg(offsets + e));
+  last = __reduce_max_sync(0xFFFFFFFFu, last);
+  const long long items = (long long)min(last, rows_max) * cols;
   const long long stride = (long long)gridDim.x * 256;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += 4 * stride) {
     uint4 v[4];
@@ -780,8 +788,9 @@ W4gGemmPlan w4g_gemm_plan(const W4gArgs& g, int num_sms) {
   return p;
 }
 
-cudaError_t launch_w4g_gather(const uint16_t* a, long long a_rows, const int32_t* rows, const int32_t* last,
-                              uint16_t* out, long long rows_max, int k, cudaStream_t stream, int num_sms) {
+cudaError_t launch_w4g_gather(const uint16_t* a, long long a_rows, const int32_t* rows, const int32_t* offsets,
+                              int experts, uint16_t* out, long long rows_max, int k, cudaStream_t stream,
+                              int num_sms) {
   const int cols = k / 8;
   const long long blocks = (rows_max * cols + 1023) / 1024;
   const long long cap = (long long)num_sms * 8;
@@ -794,8 +803,8 @@ cudaError_t launch_w4g_gather(const uint16_t* a, long long a_rows, const int32_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w4g_gather_kernel, reinterpret_cast<const uint4*>(a), rows, last,
-                            reinterpret_cast<uint4*>(out), (int)rows_max, (int)a_rows, cols);
+  return cudaLaunchKernelEx(&cfg, w4g_gather_kernel, reinterpret_cast<const uint4*>(a), rows, offsets,
+                            reinterpret_cast<uint4*>(out), (int)rows_max, (int)a_rows, experts, cols);
 }
 
 cudaError_t launch_w4g_gemm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,

@@ -140,6 +140,35 @@ def test_rows_past_the_groups_are_left(scale):
     assert bsr.device_status() == 0
 
 
+@pytest.mark.parametrize("raw", [[0, 120, 200, 150], [7, 90, 40, -3], [0, 200, 2 ** 31 - 1, 0], [-5, -1, 30, 30],
+                                 [0, 0, 0, -1]])
+@pytest.mark.parametrize("rows_max", [12, 200])
+def test_offsets_that_fall_are_clamped_with_a_row_index(raw, rows_max):
+    """An offset below the one before it stands for the one before, the last
+    one too, on the decode kernel and past it: the rows that the clamped groups
+    have are computed, the ones behind them are left."""
+    n, k, group = 70, 256, 64
+    w = make_weight(32, (3,), n, k, group, True)
+    a = make_acts(33, 50, k)
+    raw = [o * rows_max // 200 if 0 < o <= 200 else o for o in raw]
+    ends = np.minimum(np.maximum.accumulate([0] + raw[1:]), rows_max)
+    counts, used = np.diff(ends).tolist(), int(ends[-1])
+    rows = torch.randint(0, 50, (rows_max,), generator=torch.Generator().manual_seed(2), dtype=torch.int32)
+    off = torch.tensor(raw, dtype=torch.int32, device=DEV)
+    need = bsr.w4g_proj_grouped_scratch_bytes(rows_max, 3, k)
+    # scratch that holds another call's rows: NaN
+    scratch = torch.full((need,), 255, dtype=torch.uint8, device=DEV) if need else None
+    out = torch.full((rows_max, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    bsr.w4g_proj_grouped(a.to(DEV), off, *dev(w), rows=rows.to(DEV), out=out, scratch=scratch)
+    ref, mag = grouped_reference(a, counts, w, rows.numpy())
+    check(out[:used], ref, mag, k, group)
+    assert bool((out[used:] == 7.0).all())
+    plain = torch.full((rows_max, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    bsr.w4g_proj_grouped(a[rows.long()].to(DEV), off, *dev(w), out=plain)
+    assert torch.equal(out.view(torch.int16), plain.view(torch.int16))
+    assert bsr.device_status() == 0
+
+
 @pytest.mark.parametrize("m", [4, 100])
 def test_infinities_and_nan_stay_in_their_row(m):
     n, k = 100, 256
