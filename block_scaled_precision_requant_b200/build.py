@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libbsr.so")
 SOURCES = ["api.cu", "requant.cu", "decode.cu", "gemm_tc.cu", "noalloc.cu", "debug.cu", "silu.cu", "nvfp4_gemv.cu",
            "w4a4.cu", "w4a4_gemm.cu", "host_io.cu", "w4g_gemv.cu", "w4g_gemm.cu", "moe.cu", "w4g_api.cu"]
 HEADERS = ["common.cuh", "quant.cuh", "kernels.h", "nvfp4_enc.cuh", "w4a4_desc.cuh", "fp_cvt.cuh", "occupancy.h",
-           "w4g.h", "w4g_dev.cuh"]
+           "w4g.h", "w4g_dev.cuh", "w4g_ring.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -59,6 +59,7 @@
 #include "common.cuh"
 #include "w4g.h"
 #include "w4g_dev.cuh"
+#include "w4g_ring.h"
 
 namespace bsr {
 namespace {
@@ -290,12 +291,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.next(stages);
         }
       }
-      // copies of the last stages must have landed before the CTA may exit
-      if (!ok && lane == 0) {
-        const uint32_t n = (uint32_t)stages;
-        for (uint32_t j = it > n ? it - n : 0u; j < it; ++j)
-          if (!wait_drain(&ctrl->full[j % n], (j / n) & 1u)) break;
-      }
+      // the last stages' copies must have landed before the CTA may exit or, with
+      // a shared K, its stages take the other CTAs' sums, also when an unpacking
+      // warp gave up after the last issue here
+      if (lane == 0)
+        drain_ring(it, (uint32_t)stages,
+                   [&](uint32_t s, uint32_t parity) { return wait_drain(&ctrl->full[s], parity); });
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA
