@@ -49,11 +49,12 @@ inline W4gSpread w4g_spread(const W4gArgs& g) {
 }
 
 // Few rows per expert: warp-level tensor instructions fed by a streamed weight.
-// Items of rt tiles of tr (<= 16) weight rows x 8 nt activation rows, ks warps
-// along K; the codes' tensor map has boxes of tr rows x 128 bytes with the
+// Items of rt (1, 2 or 4) tiles of 16 weight rows x 8 nt activation rows, ks
+// warps along K; the codes' tensor map has boxes of a tile x 128 bytes with the
 // 128-byte swizzle.
+constexpr int kW4gGemvRows = 16;
 struct W4gGemvPlan {
-  int tr, rt, nt, ks, slots, nblk, chunks, grid;
+  int rt, nt, ks, slots, nblk, chunks, grid;
   size_t smem;
   double us;  // estimated time
 };
@@ -78,6 +79,17 @@ cudaError_t launch_w4g_gather(const uint16_t* a, long long a_rows, const int32_t
                               int num_sms);
 cudaError_t launch_w4g_gemm(const CUtensorMap& tm_q, const CUtensorMap& tm_a, const W4gArgs& g, const W4gGemmPlan& p,
                             int* status, cudaStream_t stream);
+
+// Which of the two takes a product.  `gemv` is filled where it may, `gemm`
+// always.  At most kW4gFewRows rows per expert always take the first, so that
+// they need no scratch.
+constexpr int kW4gFewRows = 4;
+struct W4gPlan {
+  bool few = false;
+  W4gGemvPlan gemv = {};
+  W4gGemmPlan gemm = {};
+};
+W4gPlan w4g_plan(const W4gArgs& g, int num_sms);
 
 // Router.  Blocks of route_block_tokens(tokens) tokens; scratch holds one
 // row of `experts` counts per block (none when there is one block).

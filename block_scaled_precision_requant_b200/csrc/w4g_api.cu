@@ -138,39 +138,23 @@ bsr_status encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, u
 }
 
 // At most this many rows never take the tensor-core kernel.
-bool few_rows(int64_t r, int64_t experts) { return r <= 4 * experts; }
+bool few_rows(int64_t r, int64_t experts) { return r <= bsr::kW4gFewRows * experts; }
 
 // One product, every check and tensor map made before its launch.  `gather`:
 // it takes its rows in order, from the buffer that the plan was given.
 struct Product {
   bsr::W4gArgs g;
-  bool few = false, gather = false;
-  bsr::W4gGemvPlan gemv;
-  bsr::W4gGemmPlan gemm;
+  bsr::W4gPlan plan;
+  bool gather = false;
   CUtensorMap q, a;
 };
 
 bsr_status plan_product(Product& p, const bsr::W4gArgs& g, uint16_t* ordered, const Device& d) {
   p.g = g;
-  // The decode kernel reads the weight at more than the tensor-core kernel's
-  // rate and splits K, but its work grows with every 8 rows of an expert; the
-  // tensor-core kernel's time is that of whole tiles.  Each plan estimates its
-  // own, and past 16 rows per expert (two tiles of the decode kernel's widest
-  // item) or 4096 in all its is never the shorter.  (Measured, us, decode /
-  // tensor-core: 14336 x 4096 at 8 rows 14.5 / 17.3, at 12 20.9 / 17.3, with
-  // groups of 32 26.9 / 27.5; 4096 x 4096 at 16 rows 10.9 / 16.4; 128 experts of
-  // 1536 x 2048 at 5 rows each 65 / 86, at 8 96 / 86, at 12 111 / 85, with groups
-  // of 32 144 / 151; 8 experts of 14336 x 4096 at 6 rows each 79 / 101, at 8 113 /
-  // 102.)
-  p.gemm = bsr::w4g_gemm_plan(g, d.num_sms);
-  p.few = few_rows(g.rows_max, g.experts);
-  if (p.few || (g.rows_max <= 16LL * g.experts && g.rows_max <= 4096)) {
-    p.gemv = bsr::w4g_gemv_plan(g, d.num_sms);
-    p.few = p.few || p.gemv.us < p.gemm.us;
-  }
+  p.plan = bsr::w4g_plan(g, d.num_sms);
   const uint64_t wrows = (uint64_t)g.experts * (uint64_t)g.n, wpitch = (uint64_t)g.k / 2;
-  if (p.few) {
-    return encode_2d(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, wpitch, wrows, wpitch, 128, (uint32_t)p.gemv.tr,
+  if (p.plan.few) {
+    return encode_2d(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, wpitch, wrows, wpitch, 128, bsr::kW4gGemvRows,
                      CU_TENSOR_MAP_SWIZZLE_128B, "w4g codes");
   }
   const bsr_status st = encode_2d(&p.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.q, wpitch, wrows, wpitch, 64, 128,
@@ -183,12 +167,12 @@ bsr_status plan_product(Product& p, const bsr::W4gArgs& g, uint16_t* ordered, co
     p.g.rows = nullptr;
   }
   return encode_2d(&p.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.g.a, (uint64_t)g.k, (uint64_t)p.g.a_rows,
-                   (uint64_t)g.k * 2, 64, (uint32_t)p.gemm.bm, CU_TENSOR_MAP_SWIZZLE_128B, "w4g activations");
+                   (uint64_t)g.k * 2, 64, (uint32_t)p.plan.gemm.bm, CU_TENSOR_MAP_SWIZZLE_128B, "w4g activations");
 }
 
 bsr_status run_product(const Product& p, const Device& d, void* stream) {
-  return cuda_status(p.few ? bsr::launch_w4g_gemv(p.q, p.g, p.gemv, d.status, as_stream(stream))
-                           : bsr::launch_w4g_gemm(p.q, p.a, p.g, p.gemm, d.status, as_stream(stream)),
+  return cuda_status(p.plan.few ? bsr::launch_w4g_gemv(p.q, p.g, p.plan.gemv, d.status, as_stream(stream))
+                                : bsr::launch_w4g_gemm(p.q, p.a, p.g, p.plan.gemm, d.status, as_stream(stream)),
                      "w4g projection launch");
 }
 
@@ -242,6 +226,31 @@ MlpLayout mlp_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t inn
 }
 
 }  // namespace
+
+namespace bsr {
+
+// The decode kernel reads the weight at more than the tensor-core kernel's
+// rate and splits K, but its work grows with every 8 rows of an expert; the
+// tensor-core kernel's time is that of whole tiles.  Each plan estimates its
+// own, and past 16 rows per expert (two tiles of the decode kernel's widest
+// item) or 4096 in all its is never the shorter.  (Measured, us, decode /
+// tensor-core: 14336 x 4096 at 8 rows 14.5 / 17.3, at 12 20.9 / 17.3, with
+// groups of 32 26.9 / 27.5; 4096 x 4096 at 16 rows 10.9 / 16.4; 128 experts of
+// 1536 x 2048 at 5 rows each 65 / 86, at 8 96 / 86, at 12 111 / 85, with groups
+// of 32 144 / 151; 8 experts of 14336 x 4096 at 6 rows each 79 / 101, at 8 113 /
+// 102.)
+W4gPlan w4g_plan(const W4gArgs& g, int num_sms) {
+  W4gPlan p;
+  p.gemm = w4g_gemm_plan(g, num_sms);
+  p.few = few_rows(g.rows_max, g.experts);
+  if (p.few || (g.rows_max <= 16LL * g.experts && g.rows_max <= 4096)) {
+    p.gemv = w4g_gemv_plan(g, num_sms);
+    p.few = p.few || p.gemv.us < p.gemm.us;
+  }
+  return p;
+}
+
+}  // namespace bsr
 
 extern "C" {
 

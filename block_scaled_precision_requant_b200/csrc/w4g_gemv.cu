@@ -16,7 +16,7 @@
 // activations are permuted to match.  A group's products are summed from zero
 // by the mma, then scaled in float32.
 //
-// Work split: an item is rt <= 4 tiles of tr <= 16 weight rows of one expert
+// Work split: an item is rt = 1, 2 or 4 tiles of 16 weight rows of one expert
 // times up to 8 NT of its activation rows; ks warps of a CTA split its K in
 // chunks of 256 (128 bytes) dealt cyclically, and add their sums in a fixed
 // order through shared memory.  The split depends on K only: a row's bits
@@ -28,7 +28,7 @@
 // us; with a CTA's warps taking consecutive items 68.7).
 //
 // One CTA per SM: 16 multiplying warps, and a producer warp whose lane w keeps
-// warp w's ring full of tiles (tr rows x 128 bytes, 128-byte swizzle, by TMA)
+// warp w's ring full of tiles (16 rows x 128 bytes, 128-byte swizzle, by TMA)
 // across chunks and items; no CTA barrier in the stream.  With the copies
 // issued by the multiplying warps themselves the same work took 17% longer (dense
 // 14336 x 4096, 1 row: 15.6 us against 13.3), and three or four smaller CTAs
@@ -72,10 +72,12 @@ static_assert(128 * kCodesRegs + 32 * kWarps * kMulRegs <= kThreads * kLaunchReg
 constexpr int kChunk = 256;       // elements of K per chunk
 constexpr int kChunkBytes = 128;  // of codes
 
-constexpr int kSlotBytes = 16 * kChunkBytes;
+constexpr int kRows = kW4gGemvRows;  // weight rows per tile: the mma's
+static_assert(kRows == 16, "mma.m16n8k16");
+constexpr int kSlotBytes = kRows * kChunkBytes;
 
 struct GemvCfg {
-  int tr, rt, ks, slots, nblk, chunks;
+  int rt, ks, slots, nblk, chunks;
   int vec;  // scales (and zero points) of a lane may be read as one vector
 };
 
@@ -136,7 +138,8 @@ struct Item {
   int row0, cnt;  // first grouped row, rows (at most 8 NT)
 };
 
-// G: group.  RT: most 16-row tiles of an item.  NT: 8-row activation tiles.
+// G: group.  RT: most 16-row tiles of an item (2: one or two; 4: four).  NT:
+// 8-row activation tiles.
 template <int G, int RT, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     w4g_gemv_kernel(const __grid_constant__ CUtensorMap tm_q, const W4gArgs g, const GemvCfg c,
@@ -172,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int items = s_pre[g.experts];
   const int step = (int)gridDim.x * ngrp;
-  const int rb = c.tr * c.rt;  // weight rows of an item
+  const int rt = RT == 4 ? 4 : c.rt;
+  const int rb = kRows * rt;  // weight rows of an item
   auto find = [&](int i) {
     const GroupTile f = find_tile(i, g.experts, TOK, s_off, s_pre);
     return Item{f.expert, f.n, f.row0, f.cnt};
@@ -198,11 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item t = find(it);
         const int y = t.e * g.n + t.blk * rb;
         for (int ch = wk; ok && ch < c.chunks; ch += c.ks)
-          for (int i = 0; i < c.rt; ++i) {
+          for (int i = 0; i < rt; ++i) {
             ok = mbar_wait(&e[slot], phase, abort_flag, status, DEV_ERR_TIMEOUT_DECODE);
             if (!ok) break;
-            mbar_arrive_expect_tx(&f[slot], (uint32_t)c.tr * kChunkBytes);
-            tma_load_2d(ring + (size_t)slot * kSlotBytes, &tm_q, &f[slot], ch * kChunkBytes, y + i * c.tr);
+            mbar_arrive_expect_tx(&f[slot], (uint32_t)kSlotBytes);
+            tma_load_2d(ring + (size_t)slot * kSlotBytes, &tm_q, &f[slot], ch * kChunkBytes, y + i * kRows);
             ++issued;
             if (++slot == c.slots) {
               slot = 0;
@@ -292,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int mrow[ML];
 #pragma unroll
   for (int l = 0; l < ML; ++l) {
-    const int tile = l * 2 + (lane >> 4), r = lane & 15;
-    mrow[l] = r < c.tr && tile < c.rt ? tile * c.tr + r : 1 << 30;
+    const int r = l * 32 + lane;
+    mrow[l] = r < rb ? r : 1 << 30;
   }
   auto load_meta = [&](const Item& t, int ch) {
     Meta m;
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase = phase0;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-          if (i < c.rt) {
+          if (i < rt) {
             if (seg == 0 && !dead) {
               const bool landed = mbar_wait(&bars[slot], phase, abort_flag, status, DEV_ERR_TIMEOUT_DECODE);
               if (__any_sync(0xFFFFFFFFu, !landed)) dead = true;
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* mine = red + (size_t)warp * PITCH * TOK;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
-      if (i < c.rt) {
+      if (i < rt) {
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
@@ -506,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float* part = red + (size_t)grp * c.ks * PITCH * TOK;
     for (int i = wk * 32 + lane; i < PITCH * t.cnt; i += bar_threads) {
       const int tok = i / PITCH, r = i & (PITCH - 1);
-      const int row = n0 + (r >> 4) * c.tr + (r & 15);
-      if ((r >> 4) >= c.rt || (r & 15) >= c.tr || row >= g.n) continue;
+      const int row = n0 + r;
+      if (r >= rb || row >= g.n) continue;
       float v = 0.0f;
       for (int w = 0; w < c.ks; ++w) v += part[((size_t)w * TOK + tok) * PITCH + r];
       reinterpret_cast<__nv_bfloat16*>(g.out)[(size_t)(t.row0 + tok) * (size_t)g.n + row] =
@@ -560,7 +564,7 @@ cudaError_t launch(const CUtensorMap& tm, const W4gArgs& g, const GemvCfg& c, in
 template <int G>
 cudaError_t launch_g(const CUtensorMap& tm, const W4gArgs& g, const W4gGemvPlan& p, int* status,
                      cudaStream_t stream) {
-  GemvCfg c = {p.tr, p.rt, p.ks, p.slots, p.nblk, p.chunks, 0};
+  GemvCfg c = {p.rt, p.ks, p.slots, p.nblk, p.chunks, 0};
   constexpr int gc = kChunk / G;  // a chunk's scales start at a multiple of gc groups of the row
   c.vec = (g.k / G) % gc == 0 && reinterpret_cast<uintptr_t>(g.scale) % (2u * gc) == 0 &&
           reinterpret_cast<uintptr_t>(g.zero) % (unsigned)gc == 0;
@@ -587,31 +591,29 @@ W4gGemvPlan w4g_gemv_plan(const W4gArgs& g, int num_sms) {
   p.nt = sp.mean <= 8.0 ? 1 : 2;
   const int tok = 8 * p.nt;
   const double tiles = sp.tiles(tok);
-  // rt tiles of tr rows per item: the least estimated time over whole waves.
+  // rt tiles of 16 rows per item: the least estimated time over whole waves.
   // Measured per wave, us: 2.3, and per chunk of a warp 0.7 (its activations and
   // scales) + 0.9 per tile (16 / 32 / 64 rows at K = 2048: 5.2 / 7.5 / 13.3, at
-  // K = 14336: 13.4 / 19 / 33).  A tile of fewer rows takes as long, so tr falls
-  // below 16 only where that saves a wave; three tiles take as long as four.
+  // K = 14336: 13.4 / 19 / 33).  (Three tiles took as long as four, tiles of
+  // fewer rows as long as full ones.)
   const double slots_all = (double)num_sms * ngrp;
   double best = 0.0;
   // (At G = 32 four tiles' scales, with two activation tiles their sums, leave
   // too little room for the ring.)
-  for (int rt = g.group == 32 || p.nt == 2 ? 2 : 4; rt >= 1; --rt)
-    for (int tr = 16; tr >= 8; --tr) {
-      const double items = (double)((g.n + rt * tr - 1) / (rt * tr)) * tiles;
-      const double cost = ceil(items / slots_all) * (2.3 + per_warp * (0.7 + 0.9 * (rt == 3 ? 4 : rt)));
-      if (best == 0.0 || cost < best - 1e-9) {
-        best = cost;
-        p.rt = rt;
-        p.tr = tr;
-      }
+  for (int rt = g.group == 32 || p.nt == 2 ? 2 : 4; rt >= 1; rt /= 2) {
+    const double items = (double)((g.n + rt * kRows - 1) / (rt * kRows)) * tiles;
+    const double cost = ceil(items / slots_all) * (2.3 + per_warp * (0.7 + 0.9 * rt));
+    if (best == 0.0 || cost < best - 1e-9) {
+      best = cost;
+      p.rt = rt;
     }
+  }
   // The call: a launch, and by group and activation tiles (measured, us, 14336 x
   // 4096, estimate before factors 10.9, at groups of 32 and two activation tiles
   // 14.6: groups of 128 13.6, two tiles 21.0; 64 15.3 and 21.6; 32 17.5 and 27).
   const double f = p.nt == 1 ? (g.group == 64 ? 1.15 : 1.0) : (g.group == 32 ? 1.65 : 1.25);
   p.us = 2.7 + best * f;
-  const int rb = p.rt * p.tr;
+  const int rb = p.rt * kRows;
   p.nblk = (g.n + rb - 1) / rb;
   // slots: as many as the shared memory of an SM (227 KB) has room for.  A
   // chunk's tiles stay until its last segment.
