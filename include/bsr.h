@@ -429,8 +429,9 @@ bsr_status bsr_proj_silu(const uint16_t* gate, const uint16_t* up, const int8_t*
  * The experts' weights of one projection are stacked: codes [E, N, K/2],
  * scales [E, N, K/G], zero points [E, N, K/G].  Zero points above 15 are
  * outside the contract (results unspecified).  For given sizes, a call's output
- * bits do not depend on scheduling; another number of rows may take another
- * kernel, which adds the groups in another order.  Inputs, outputs and scratch
+ * bits do not depend on scheduling; another number of rows, or a row index
+ * where there was none, may take another kernel, which adds the groups in
+ * another order.  Inputs, outputs and scratch
  * must not overlap except where stated; calls that may run at the same time
  * need scratch of their own.
  */
