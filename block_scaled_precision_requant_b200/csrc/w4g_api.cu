@@ -201,6 +201,11 @@ bsr_status check_logits(const char* who, const void* logits, int logits_type, un
 struct MlpLayout {
   size_t ids, weights, offsets, rows, pos, route, ordered, gate, up, hidden, down, total;
 };
+// Its size stays below 2^62 bytes (and a little): the rows alone are 2 (3 inner +
+// 2 k) bytes per pair.
+bool mlp_fits(int64_t tokens, int64_t top_k, int64_t inner, int64_t k) {
+  return tokens * top_k <= (int64_t(1) << 61) / (3 * inner + 2 * k);
+}
 MlpLayout mlp_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner, int64_t k) {
   const size_t pairs = (size_t)tokens * (size_t)top_k;
   MlpLayout L;
@@ -368,7 +373,7 @@ bsr_status bsr_moe_combine(const uint16_t* y, int64_t y_rows, const int32_t* pos
 size_t bsr_w4g_moe_mlp_scratch_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner, int64_t k) {
   if (tokens <= 0 || experts < 1 || experts > bsr::kRouteMaxExperts || top_k < 1 || top_k > experts ||
       top_k > bsr::kRouteMaxTopK || tokens > BSR_W4G_MAX_DIM / top_k || !dim_ok(inner) || !dim_ok(k) || inner == 0 ||
-      k == 0)
+      k == 0 || !mlp_fits(tokens, top_k, inner, k))
     return 0;
   return mlp_layout(tokens, experts, top_k, inner, k).total;
 }
@@ -386,6 +391,9 @@ bsr_status bsr_w4g_moe_mlp(const uint16_t* x, const void* logits, int logits_typ
   if (!dim_ok(inner) || !dim_ok(k) || experts > BSR_W4G_MAX_DIM / inner || experts > BSR_W4G_MAX_DIM / k)
     return report(BSR_EINVAL, "%s: dimension out of range (inner=%lld k=%lld; experts times each <= 2^31 - 256)", who,
                   (long long)inner, (long long)k);
+  if (!mlp_fits(tokens, top_k, inner, k))
+    return report(BSR_EINVAL, "%s: scratch of 2^62 bytes or more (tokens=%lld top_k=%lld inner=%lld k=%lld)", who,
+                  (long long)tokens, (long long)top_k, (long long)inner, (long long)k);
   if (tokens == 0) return ok();
   if ((st = check_logits(who, logits, logits_type, flags)) != BSR_OK) return st;
   if (!x || !out) return report(BSR_EINVAL, "%s: null pointer", who);

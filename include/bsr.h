@@ -528,7 +528,7 @@ bsr_status bsr_moe_combine(const uint16_t* y, int64_t y_rows, const int32_t* pos
  * other.  x, residual (or NULL) and out are [T, K] BF16; out may be residual,
  * not x.  The three weights need not share a group or scale type.  Scratch
  * (device, 256-byte aligned) of bsr_w4g_moe_mlp_scratch_bytes bytes (0 for
- * invalid sizes).  Every check that can fail comes before the first launch.
+ * invalid sizes, which those are whose scratch would take 2^62 bytes).  Every check that can fail comes before the first launch.
  */
 size_t bsr_w4g_moe_mlp_scratch_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner, int64_t k);
 bsr_status bsr_w4g_moe_mlp(const uint16_t* x, const void* logits, int logits_type, const bsr_w4g_weight* gate,

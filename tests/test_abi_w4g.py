@@ -164,3 +164,21 @@ def test_sizes_near_31_bits_are_refused(L):
     w = weight(group=32)
     assert L.bsr_w4g_moe_mlp(A, A, 0, w, w, w, None, A, 4, 8, 2, 0, top // 8 + 32, 64, A, 0, None) == EINVAL
     assert L.bsr_w4g_moe_mlp_scratch_bytes(4, 8, 2, big, 64) == 0
+
+
+def test_mlp_scratch_past_64_bits_is_refused(L):
+    """Sizes that each hold but whose scratch bytes pass 64 bits: no wrapped
+    size, and the call refuses them before it looks at the scratch."""
+    top, group = 2 ** 31 - 256, weight(group=32)
+
+    def call(t, e, k, inner, hidden):
+        return L.bsr_w4g_moe_mlp(A, A, 0, group, group, group, None, A, t, e, k, 0, inner, hidden, A, 2 ** 64 - 1, None)
+
+    for t, e, k, inner, hidden in ((top, 1, 1, top, 32), (top, 1, 1, top, top), (2 ** 30, 1, 1, top, top),
+                                   (top // 2, 2, 2, top // 2 - 64, 64), (top, 1, 1, 2 ** 30, 2 ** 30)):
+        assert L.bsr_w4g_moe_mlp_scratch_bytes(t, e, k, inner, hidden) == 0
+        assert call(t, e, k, inner, hidden) == EINVAL and "scratch" in bsr.last_error()
+    for t, e, k, inner, hidden in ((2 ** 26 - 8, 32, 32, 2 ** 26 - 32, 2 ** 26 - 32), (2 ** 20, 1, 1, top, top)):
+        pairs = t * k
+        least = pairs * 2 * (3 * inner + 2 * hidden)
+        assert least <= L.bsr_w4g_moe_mlp_scratch_bytes(t, e, k, inner, hidden) <= least + 2 ** 37
