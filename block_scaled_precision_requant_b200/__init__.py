@@ -811,7 +811,7 @@ def _like(t, name, stream):
     allocates belongs to the stream that uses it."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+        raise _not_a_tensor(t, name)
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -856,7 +856,9 @@ def _w4g_weight(w_q, w_scale, w_zero, lead, n, k, index, name):
     (n, k/G)`` bfloat16 or float16, zero points (or None) like the scales,
     uint8."""
     torch = _torch()
-    if not isinstance(w_scale, torch.Tensor) or w_scale.dim() != len(lead) + 2:
+    if not isinstance(w_scale, torch.Tensor):
+        raise _not_a_tensor(w_scale, f"{name} scale")
+    if w_scale.dim() != len(lead) + 2:
         raise ValueError(f"{name} scale must be a tensor of {len(lead) + 2} dimensions")
     groups = w_scale.shape[-1]
     if groups == 0 or k % groups or k // groups not in (32, 64, 128):
@@ -874,8 +876,15 @@ def _w4g_weight(w_q, w_scale, w_zero, lead, n, k, index, name):
     )
 
 
+def _not_a_tensor(t, name):
+    return TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+
+
 def _dims(t, count, name):
-    shape = t.shape
+    try:
+        shape = t.shape
+    except AttributeError:
+        raise _not_a_tensor(t, name) from None
     if len(shape) != count:
         raise ValueError(f"{name} must have {count} dimensions, got shape {tuple(shape)}")
     return shape
@@ -887,6 +896,8 @@ def _scratch(scratch, need, like):
         if not need:
             return None, 0
         scratch = like.new_empty((need,), dtype=_torch().uint8)
+    elif not isinstance(scratch, _torch().Tensor):
+        raise _not_a_tensor(scratch, "scratch")
     elif scratch.get_device() != like.get_device():
         raise ValueError(f"scratch must be on {like.device}")
     elif not scratch.is_contiguous():
@@ -1038,6 +1049,9 @@ def w4g_moe_mlp(x, logits, gate, up, down, top_k: int, renormalize: bool = True,
     index, here = _like(x, "x", stream)
     tokens, k = _dims(x, 2, "x")
     experts = _dims(logits, 2, "logits")[1]
+    for w, name in ((gate, "gate"), (up, "up"), (down, "down")):
+        if not isinstance(w, (tuple, list)) or len(w) != 3:
+            raise TypeError(f"{name} must be (codes, scale, zero points or None)")
     inner = _dims(gate[0], 3, "gate codes")[1]
     x_ptr = _ptr(x, bf16, (tokens, k), "x", index)
     kind = _logits_type(logits)

@@ -182,3 +182,30 @@ def test_mlp_scratch_past_64_bits_is_refused(L):
         pairs = t * k
         least = pairs * 2 * (3 * inner + 2 * hidden)
         assert least <= L.bsr_w4g_moe_mlp_scratch_bytes(t, e, k, inner, hidden) <= least + 2 ** 37
+
+
+@pytest.mark.parametrize("bad", [[[1.0, 2.0]], None, 3])
+def test_what_is_not_a_tensor_is_a_type_error(bad, monkeypatch):
+    """Every tensor argument, whichever is looked at first; CPU tensors stand
+    in for the device's."""
+    monkeypatch.setattr(bsr, "_like", lambda t, name, stream: (-1, bsr._HERE))
+    a = torch.zeros(2, 64, dtype=torch.bfloat16)
+    q, s = torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.bfloat16)
+    e3, off = (q[None], s[None], None), torch.zeros(2, dtype=torch.int32)
+    lg, pos, wt = torch.zeros(2, 1), torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1)
+    calls = [lambda: bsr.w4g_proj(a, bad, s), lambda: bsr.moe_route(bad, 1), lambda: bsr.moe_combine(bad, pos, wt),
+             lambda: bsr.moe_combine(a, bad, wt), lambda: bsr.moe_combine(a, pos, bad),
+             lambda: bsr.w4g_proj_grouped(a, off, bad, s), lambda: bsr.w4g_moe_mlp(bad, lg, e3, e3, e3, 1),
+             lambda: bsr.w4g_moe_mlp(a, bad, e3, e3, e3, 1), lambda: bsr.w4g_moe_mlp(a, lg, bad, e3, e3, 1),
+             lambda: bsr.w4g_moe_mlp(a, lg, e3, bad, e3, 1), lambda: bsr.w4g_moe_mlp(a, lg, e3, e3, bad, 1),
+             lambda: bsr.w4g_moe_mlp(a, lg, (bad, s, None), e3, e3, 1),
+             lambda: bsr.w4g_moe_mlp(a, lg, (q[None], bad, None), e3, e3, 1)]
+    if bad is not None:  # stands for every row in order, zero points of 8, memory of the call's own
+        calls += [lambda: bsr.w4g_proj_grouped(a, off, q[None], s[None], rows=bad), lambda: bsr.w4g_proj(a, q, s, bad),
+                  lambda: bsr._scratch(bad, 8, a)]
+    for call in calls:
+        with pytest.raises(TypeError, match="must be"):
+            call()
+    for short in ((q[None], s[None]), (q[None], s[None], None, None)):
+        with pytest.raises(TypeError, match="gate must be"):
+            bsr.w4g_moe_mlp(a, lg, short, e3, e3, 1)
