@@ -956,7 +956,8 @@ def w4g_proj_grouped(a, offsets, w_q, w_scale, w_zero=None, rows=None, out=None,
 
 
 class MoeRoute(NamedTuple):
-    """Result of :func:`moe_route`."""
+    """Result of :func:`moe_route`.  The five are parts of one allocation: one
+    that is kept keeps the memory of all; clone what is to live longer."""
 
     ids: Any  # [T, top_k] int32: expert of each slot, -1 where none is left
     weights: Any  # [T, top_k] float32, 0 where the id is -1

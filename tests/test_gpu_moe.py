@@ -227,3 +227,21 @@ def test_refusals():
     y = torch.zeros(8, 16, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(TypeError):
         bsr.moe_combine(y, torch.zeros(4, 2, device=DEV), torch.zeros(4, 2, device=DEV))
+
+
+@pytest.mark.parametrize("t,e,k,inner,hidden,group", [(1700, 4, 2, 1504, 544, 32), (1500, 6, 3, 1088, 640, 64),
+                                                      (700, 1024, 8, 64, 96, 32), (20, 1024, 8, 128, 128, 128)])
+def test_mlp_of_large_tiles_and_many_experts(t, e, k, inner, hidden, group):
+    """The bits of the calls one by one, with a residual, zero points, FP16
+    scales, masked experts and weights over all of them."""
+    gate, up = (dev(make_weight(s, (e,), inner, hidden, group, True, s == 2)) for s in (1, 2))
+    down = dev(make_weight(3, (e,), hidden, inner, 32, False, True))
+    x, res = make_acts(4, t, hidden).to(DEV), make_acts(5, t, hidden).to(DEV)
+    logits = make_logits(6, t, e, bf16=True).to(DEV)
+    for renorm, r in ((True, res), (False, None)):
+        out = bsr.w4g_moe_mlp(x, logits, gate, up, down, k, renormalize=renorm, residual=r)
+        want = mlp_steps(x, logits, gate, up, down, k, renorm, r)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        left = out[t // 2]  # a token that no expert takes
+        assert torch.equal(left, torch.zeros_like(left) if r is None else r[t // 2])
+    assert bsr.device_status() == 0
