@@ -24,7 +24,7 @@
 //
 // Bound by latency: the chain of top_k warp reductions and the second launch,
 // with one block of 32 warps per SM.  Measured: 33 tokens of 64 experts, top
-// 8, 7.0 us; 16384 tokens of 128 experts, top 8, 22.8 us (4 tokens per warp;
+// 8, 7.2 us; 16384 tokens of 128 experts, top 8, 23 us (4 tokens per warp;
 // their 4 MB of logits take 0.7 us to read).
 //
 // Combine: out[t, :] = bf16(residual[t, :] + sum_j w[t, j] * y[pos[t, j], :]),

@@ -239,11 +239,13 @@ namespace bsr {
 // tensor-core kernel's time is that of whole tiles.  Each plan estimates its
 // own, and past 16 rows per expert (two tiles of the decode kernel's widest
 // item) or 4096 in all its is never the shorter.  (Measured, us, decode /
-// tensor-core: 14336 x 4096 at 8 rows 14.5 / 17.3, at 12 20.9 / 17.3, with
-// groups of 32 26.9 / 27.5; 4096 x 4096 at 16 rows 10.9 / 16.4; 128 experts of
-// 1536 x 2048 at 5 rows each 65 / 86, at 8 96 / 86, at 12 111 / 85, with groups
-// of 32 144 / 151; 8 experts of 14336 x 4096 at 6 rows each 79 / 101, at 8 113 /
-// 102.)
+// tensor-core: 14336 x 4096 at 8 rows 14.0 / 17.5, at 12 21.0 / 17.6, with
+// groups of 32 24.7 / 27.7; 4096 x 4096 at 8 rows 8.3 / 9.2, at 12 9.9 / 9.2; 128
+// experts of 1536 x 2048 at 5 rows each 64 / 87, at 8 99 / 87, with groups of 32
+// 117 / 151; 8 experts of 14336 x 4096 at 6 rows each 75 / 104, at 8 116 / 103.
+// The estimates miss by up to 15% beside the crossover: 2048 x 2048 at 8 rows
+// takes the tensor cores, 5.2 / 6.0, the 128 experts with groups of 32 at 12 rows
+// each too, 132 / 150.)
 W4gPlan w4g_plan(const W4gArgs& g, int num_sms) {
   W4gPlan p;
   p.gemm = w4g_gemm_plan(g, num_sms);

@@ -33,7 +33,7 @@
 // A dense product of few tiles leaves most SMs without one; clusters of 2, 4 or
 // 8 CTAs then share a tile's K, and the first adds the others' float32 sums, in
 // their order, from its own shared memory (17 rows of 4096 x 4096: 16.2 us with
-// 32 CTAs, 9.1 with clusters of 4; 64 rows of 4096 x 14336: 49.9 and 19.5).
+// 32 CTAs, 9.0 with clusters of 4; 64 rows of 4096 x 14336: 49.5 and 19.6).
 //
 // Warps (20): 0 TMA loads, 1 MMAs (one elected lane; owns the tensor memory),
 // 2-3 idle, 4-11 unpack (warp w: lanes 32 (w % 4).., half of each stage's K),
@@ -42,12 +42,13 @@
 // loop; copies and MMAs in flight are drained (bounded) before the tensor
 // memory is freed.
 //
-// Measured, 2048 x 14336 x 4096: G = 128 192-199 us = 1210-1250 TFLOP/s (the
-// MMAs and the power limit: without the MMAs the rest takes 137 us), G = 64
-// 229-257 us = 940-1050, G = 32 365-379 us = 635-660 TFLOP/s (the epilogue's
-// chain of wait, load and FMAs per group, about 520 cycles; no pipe is above
-// 42%).  Narrow tiles are bound by the unpacking and the MMA warp's fixed work
-// per group: 50 rows 17 us.  Tried and slower: 16 epilogue warps (G = 32 457 ->
+// Measured, 2048 x 14336 x 4096, in short runs: G = 128 192-196 us = 1230-1250
+// TFLOP/s, G = 64 225-235 us = 1020-1070, G = 32 366-377 us = 640-657; for
+// seconds on end, under the power limit of 1000 W: 219 us at 1575 MHz, 260 at
+// 1700, 366 at 1965.  G = 128 is bound by the MMAs and that limit (without the
+// MMAs the rest takes 137 us), G = 32 by the epilogue's chain of wait, load and
+// FMAs per group, about 520 cycles (no pipe is above 42%).  Narrow tiles are bound by the unpacking and the MMA warp's fixed work
+// per group: 50 rows 18 us.  Tried and slower: 16 epilogue warps (G = 32 457 ->
 // 620 us), two warps that issue MMAs (190 -> 206); no faster: a third buffer at
 // BM = 128, the epilogue's loads a chunk ahead within a group (more than 16
 // columns of them spill) or across groups.

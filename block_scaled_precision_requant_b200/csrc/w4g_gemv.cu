@@ -39,13 +39,13 @@
 // are read a chunk ahead and kept as stored until they are staged in shared
 // memory: converting them at the load would wait for it.
 //
-// Measured (inputs larger than L2): 14336 x 4096, groups of 128: 1 row 12.9
-// us = 2.3 TB/s, 8 rows 14.5 us; five or six experts of that size (4 tokens,
-// top 2 of 8) 44 us = 3.8 TB/s; 122 experts of 1536 x 2048 (48 tokens, top 8
-// of 128, groups of 64, zero points) 70.5 us = 3.0 TB/s.  With the
+// Measured (inputs larger than L2): 14336 x 4096, groups of 128: 1 row 12.5
+// us = 2.4 TB/s, 8 rows 14.1 us; five or six experts of that size (4 tokens,
+// top 2 of 8) 43.4 us = 3.8 TB/s; 122 experts of 1536 x 2048 (48 tokens, top 8
+// of 128, groups of 64, zero points) 67.4 us = 3.1 TB/s.  With the
 // multiplication taken out the stream alone reaches 5.25 TB/s: the kernel is
-// bound by issue and instruction latency (about 21 instructions per word and
-// warp, 57% of the issue slots with 4 warps per scheduler; without the
+// bound by issue and instruction latency (about 20 instructions per word and
+// warp, 54% of the issue slots with 4 warps per scheduler; without the
 // unpacking's FMAs, 22% of all instructions, it is 9% faster), at one or two
 // waves also by the launch and the first bytes.
 #include <cuda_bf16.h>
